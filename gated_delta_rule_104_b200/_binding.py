@@ -18,15 +18,16 @@ LIB_PATH = os.environ.get("DELTALOG_LIBRARY") or os.path.join(HERE, "libdeltalog
 GUARD_LIB_PATH = os.path.join(HERE, "libdeltalog_guard.so")
 
 DL_OK, DL_ERR_INVALID_ARG, DL_ERR_UNSUPPORTED, DL_ERR_LOG_FULL, DL_ERR_CUDA = range(5)
-DL_F32, DL_BF16, DL_I8 = 0, 1, 2
+DL_F32, DL_BF16, DL_I8, DL_E4M3 = 0, 1, 2, 3
 DL_DECAY_HEAD, DL_DECAY_CHANNEL, DL_RWKV6 = 0, 1, 2
 DL_MAX_LOG = 64
-ABI_VERSION = 9
+ABI_VERSION = 10
 
 EXPORTS = ("dl_gdn_decode_step", "dl_kda_decode_step", "dl_rwkv6_decode_step", "dl_log_append_read", "dl_log_merge",
            "dl_log_merge_read", "dl_log_work_bytes", "dl_log_append_read_noalloc", "dl_pool_step",
            "dl_pool_flush", "dl_state_bytes", "dl_state_to_i8", "dl_state_from_i8", "dl_status_string",
-           "dl_last_error", "dl_abi_version", "dl_device_faults", "dl_index_guard_build")
+           "dl_last_error", "dl_abi_version", "dl_device_faults", "dl_index_guard_build", "dl_rms_norm",
+           "dl_rows_from_8bit", "dl_conv_prompt", "dl_conv_step", "dl_ssm_prompt", "dl_ssm_step", "dl_ssm_work_bytes")
 DL_NOALLOC_WORK_BYTES = 16 << 20
 
 
@@ -45,6 +46,19 @@ class dl_log(ctypes.Structure):
 class dl_pool(ctypes.Structure):
     _fields_ = [("S", ctypes.c_void_p), ("s_dtype", ctypes.c_int), ("P", ctypes.c_int), ("n", ctypes.c_void_p),
                 ("status", ctypes.c_void_p), ("log", dl_log)]
+
+
+class dl_conv(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("channels", ctypes.c_int), ("taps", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("silu", ctypes.c_int)]
+
+
+class dl_ssm(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_longlong), ("dt", ctypes.c_void_p),
+                ("dt_stride", ctypes.c_longlong), ("b", ctypes.c_void_p), ("b_stride", ctypes.c_longlong),
+                ("c", ctypes.c_void_p), ("c_stride", ctypes.c_longlong), ("z", ctypes.c_void_p),
+                ("z_stride", ctypes.c_longlong), ("A", ctypes.c_void_p), ("D", ctypes.c_void_p),
+                ("dt_bias", ctypes.c_void_p), ("dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -80,6 +94,18 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     for name in ("dl_gdn_decode_step", "dl_kda_decode_step", "dl_rwkv6_decode_step", "dl_log_append_read",
                  "dl_log_merge", "dl_log_merge_read", "dl_log_append_read_noalloc", "dl_pool_step",
                  "dl_pool_flush", "dl_state_to_i8", "dl_state_from_i8"):
+        getattr(lib, name).restype = ctypes.c_int
+    ll, sz = ctypes.c_longlong, ctypes.c_size_t
+    cp, mp = ctypes.POINTER(dl_conv), ctypes.POINTER(dl_ssm)
+    lib.dl_rms_norm.argtypes = [vp, i, ll, vp, vp, i, vp, i, ctypes.c_float, vp, i, vp, i, ll, i, vp]
+    lib.dl_rows_from_8bit.argtypes = [vp, i, vp, i, vp, i, ll, i, vp]
+    lib.dl_conv_prompt.argtypes = [cp, vp, ll, i, vp, i, vp, i, vp, vp, vp, vp]
+    lib.dl_conv_step.argtypes = [cp, vp, ll, i, vp, i, vp, vp, vp, vp]
+    lib.dl_ssm_prompt.argtypes = [vp, i, i, vp, vp, mp, vp, i, i, vp, i, i, i, i, vp, sz, vp]
+    lib.dl_ssm_step.argtypes = [vp, i, i, vp, vp, mp, vp, i, i, i, i, i, vp]
+    lib.dl_ssm_work_bytes.argtypes = [i, i, i, i, i]
+    lib.dl_ssm_work_bytes.restype = sz
+    for name in ("dl_rms_norm", "dl_rows_from_8bit", "dl_conv_prompt", "dl_conv_step", "dl_ssm_prompt", "dl_ssm_step"):
         getattr(lib, name).restype = ctypes.c_int
     lib.dl_status_string.argtypes = [ctypes.c_int]
     lib.dl_status_string.restype = ctypes.c_char_p
@@ -430,3 +456,184 @@ def dl_pool_flush(pool: Pool, slot, stream=None) -> None:
     ps = pool.struct()
     status = load().dl_pool_flush(ctypes.byref(ps), pool.log.kind, _slots(slot, B), B, H, dk, dv, _stream(stream))
     check("dl_pool_flush", status)
+
+
+# ------------------------------------------------------------------ norm, short convolution, selective scan
+
+def _rows(t, name: str, shape):
+    """Pointer and row stride of a CUDA tensor of the given shape whose rows (all
+    dimensions but the first) are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    n = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != n:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        n *= size
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(n, 1))
+
+
+def _full(t, name: str, shape, dtype=None, optional: bool = False) -> Optional[int]:
+    """Pointer of a contiguous CUDA tensor of the given shape (and dtype)."""
+    if t is None and optional:
+        return None
+    p = _ptr(t, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return p
+
+
+def _same_device(first, *rest) -> None:
+    """Every tensor on the current device (the stream's): a call launches there."""
+    dev = _torch().cuda.current_device() if first.is_cuda else -1
+    for t in (first, *rest):
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every operand must be a CUDA tensor")
+        if t.device.index != dev:
+            raise ValueError(f"a tensor lies on {t.device}, but the current device is cuda:{dev}")
+
+
+def _code8(t) -> int:
+    torch = _torch()
+    if t.dtype == torch.int8:
+        return DL_I8
+    if t.dtype == torch.float8_e4m3fn:
+        return DL_E4M3
+    raise TypeError(f"unsupported dtype {t.dtype} (int8 or float8_e4m3fn)")
+
+
+def dl_rms_norm(x, weight, eps: float, y, residual=None, residual_out=None, scale=None, group: int = 0,
+                stream=None) -> None:
+    """y = h / sqrt(mean(h^2) + eps) * weight over the rows of x [rows, width]
+    (rows may be strided), h = x or, with ``residual``, x + residual, which
+    ``residual_out`` receives (it may be ``residual``). y is float32, bfloat16, or
+    int8 / float8_e4m3fn codes with float32 ``scale`` [rows] (``group`` 0) or
+    [rows, ceil(width / 128)] (``group`` 128)."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, width]")
+    rows, width = x.shape
+    coded = y.dtype in (torch.int8, torch.float8_e4m3fn)
+    if coded and scale is None:
+        raise ValueError("an 8-bit y needs a scale")
+    if coded and scale.numel() != rows * (-(-width // group) if group else 1):
+        raise ValueError(f"scale has {scale.numel()} elements, expected rows x groups")
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out go together")
+    if residual is not None and residual.dtype != residual_out.dtype:
+        raise TypeError("residual and residual_out must share one dtype")
+    if scale is not None and scale.dtype != torch.float32:
+        raise TypeError("scale must be float32")
+    _same_device(x, weight, y, residual, residual_out, scale)
+    xp, xs = _rows(x, "x", (rows, width))
+    args = (xp, _dtype_code(x), xs, _full(residual, "residual", (rows, width), optional=True),
+            _full(residual_out, "residual_out", (rows, width), optional=True),
+            DL_F32 if residual is None else _dtype_code(residual), _full(weight, "weight", (width,)), _dtype_code(weight),
+            float(eps), _full(y, "y", (rows, width)), _code8(y) if coded else _dtype_code(y),
+            _ptr(scale, "scale", True), int(group), rows, width, _stream(stream))
+    check("dl_rms_norm", load().dl_rms_norm(*args))
+
+
+def dl_rows_from_8bit(codes, scale, out, group: int = 0, stream=None) -> None:
+    """The values code * scale of dl_rms_norm's 8-bit rows into ``out`` (float32 or bfloat16)."""
+    if codes.dim() != 2:
+        raise ValueError("codes must be [rows, width]")
+    rows, width = codes.shape
+    if scale.numel() != rows * (-(-width // group) if group else 1):
+        raise ValueError(f"scale has {scale.numel()} elements, expected rows x groups")
+    if scale.dtype != _torch().float32:
+        raise TypeError("scale must be float32")
+    _same_device(codes, scale, out)
+    args = (_full(codes, "codes", (rows, width)), _code8(codes), _ptr(scale, "scale"), int(group),
+            _full(out, "out", (rows, width)), _dtype_code(out), rows, width, _stream(stream))
+    check("dl_rows_from_8bit", load().dl_rows_from_8bit(*args))
+
+
+def _index(t, name: str, n: int, optional: bool) -> Optional[int]:
+    return _full(t, name, (n,), _torch().int32, optional)
+
+
+def _conv(x, w, bias, state, y, silu):
+    if x.dim() != 2 or w.dim() != 2 or state.dim() != 3:
+        raise ValueError("x must be [rows, channels], w [channels, taps], state [P, taps - 1, channels]")
+    rows, channels = x.shape
+    taps, P = w.shape[1], state.shape[0]
+    dt = _in_dtype(x, w, bias, state, y)
+    cv = dl_conv(_full(w, "w", (channels, taps)), _full(bias, "bias", (channels,), optional=True), channels, taps, dt,
+                 1 if silu else 0)
+    xp, xs = _rows(x, "x", (rows, channels))
+    return cv, xp, xs, rows, _full(state, "state", (P, taps - 1, channels)), P, _full(y, "y", (rows, channels))
+
+
+def dl_conv_prompt(x, w, bias, state, seq_start, slot, y, silu: bool = True, status=None, stream=None) -> None:
+    """Short causal convolution over ragged prompts: x [T, channels] (rows may be
+    strided), w [channels, taps], bias [channels] or None, state [P, taps - 1,
+    channels] (each slot's last inputs, read and replaced), seq_start [n + 1]
+    int32, slot [n] int32 or None, y [T, channels]."""
+    cv, xp, xs, T, sp, P, yp = _conv(x, w, bias, state, y, silu)
+    n = seq_start.numel() - 1
+    _same_device(x, w, bias, state, seq_start, slot, y, status)
+    st = load().dl_conv_prompt(ctypes.byref(cv), xp, xs, T, _index(seq_start, "seq_start", n + 1, False), n, sp, P,
+                               _index(slot, "slot", n, True), _index(status, "status", 1, True), yp, _stream(stream))
+    check("dl_conv_prompt", st)
+
+
+def dl_conv_step(x, w, bias, state, slot, y, silu: bool = True, status=None, stream=None) -> None:
+    """The convolution of one new token per sequence: x, y [B, channels], slot [B] int32 or None."""
+    cv, xp, xs, B, sp, P, yp = _conv(x, w, bias, state, y, silu)
+    _same_device(x, w, bias, state, slot, y, status)
+    st = load().dl_conv_step(ctypes.byref(cv), xp, xs, B, sp, P, _index(slot, "slot", B, True),
+                             _index(status, "status", 1, True), yp, _stream(stream))
+    check("dl_conv_step", st)
+
+
+def _ssm(S, x, dt, A, b, c, y, D, dt_bias, z):
+    P, H, dk, dv = _dims(S)
+    if x.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [rows, H, d_v], b and c [rows, G, d_k]")
+    f32 = _torch().float32
+    rows, G = x.shape[0], b.shape[1]
+    code = _in_dtype(x, dt, b, c, y, z)
+    zp, zs = _rows(z, "z", (rows, H, dv)) if z is not None else (None, 0)
+    m = dl_ssm(*_rows(x, "x", (rows, H, dv)), *_rows(dt, "dt", (rows, H)), *_rows(b, "b", (rows, G, dk)),
+               *_rows(c, "c", (rows, G, dk)), zp, zs, _full(A, "A", (H,), f32), _full(D, "D", (H,), f32, True),
+               _full(dt_bias, "dt_bias", (H,), f32, True), code)
+    return m, P, H, G, dk, dv, rows, _full(y, "y", (rows, H, dv))
+
+
+def dl_ssm_work_bytes(T: int, n_seq: int, H: int, d_k: int, d_v: int) -> int:
+    """Bytes of workspace dl_ssm_prompt needs (0 if none)."""
+    return int(load().dl_ssm_work_bytes(int(T), int(n_seq), int(H), int(d_k), int(d_v)))
+
+
+def dl_ssm_prompt(S, seq_start, slot, x, dt, A, b, c, y, D=None, dt_bias=None, z=None, work=None, status=None,
+                  stream=None) -> None:
+    """Selective scan over ragged prompts from and into the slots' states S
+    [P, H, d_v, d_k] (float32 or bfloat16): x, y (and the gate z) [T, H, d_v], dt
+    [T, H], b, c [T, G, d_k] (rows may be strided; y is contiguous), A, D, dt_bias
+    [H] float32, seq_start [n + 1] int32, slot [n] int32 or None, work a tensor of
+    dl_ssm_work_bytes(T, n, H, d_k, d_v) bytes."""
+    m, P, H, G, dk, dv, T, yp = _ssm(S, x, dt, A, b, c, y, D, dt_bias, z)
+    n = seq_start.numel() - 1
+    wp, wb = (_ptr(work, "work"), work.numel() * work.element_size()) if work is not None and work.numel() else (None, 0)
+    _same_device(S, seq_start, slot, x, dt, A, b, c, y, D, dt_bias, z, work, status)
+    st = load().dl_ssm_prompt(_ptr(S, "S"), _dtype_code(S), P, _index(slot, "slot", n, True),
+                              _index(status, "status", 1, True), ctypes.byref(m),
+                              _index(seq_start, "seq_start", n + 1, False), n, T, yp, H, G, dk, dv, wp, wb,
+                              _stream(stream))
+    check("dl_ssm_prompt", st)
+
+
+def dl_ssm_step(S, slot, x, dt, A, b, c, y, D=None, dt_bias=None, z=None, status=None, stream=None) -> None:
+    """The scan of one new token per sequence: x, y (z) [B, H, d_v], dt [B, H], b, c [B, G, d_k], slot [B] int32 or None."""
+    m, P, H, G, dk, dv, B, yp = _ssm(S, x, dt, A, b, c, y, D, dt_bias, z)
+    _same_device(S, slot, x, dt, A, b, c, y, D, dt_bias, z, status)
+    st = load().dl_ssm_step(_ptr(S, "S"), _dtype_code(S), P, _index(slot, "slot", B, True),
+                            _index(status, "status", 1, True), ctypes.byref(m), yp, B, H, G, dk, dv, _stream(stream))
+    check("dl_ssm_step", st)

@@ -24,7 +24,7 @@ dl_status ok() {
     return DL_OK;
 }
 
-size_t elem_size(dl_dtype t) { return t == DL_BF16 ? 2 : 4; }
+size_t elem_size(dl_dtype t) { return t == DL_BF16 ? 2 : t == DL_F32 ? 4 : 1; }
 bool valid_dtype(int t) { return t == DL_F32 || t == DL_BF16; }
 bool valid_state_dtype(int t) { return t == DL_F32 || t == DL_BF16 || t == DL_I8; }
 // Bytes of BH heads of d_v x d_k state (DL_I8: codes, then a float scale per row).
@@ -359,6 +359,206 @@ dl_status dl_state_from_i8(const void *S_i8, void *S, dl_dtype s_dtype, int B, i
     if (s != DL_OK) return s;
     return cuda_status(dl::launch_from_i8(S_i8, S, s_dtype, (long long)B * H * d_v, d_k, stream),
                        "from-int8 launch");
+}
+
+// ------------------------------------------------------------------ norm, short convolution, selective scan
+
+// Bytes spanned by `rows` rows of `width` elements, `stride` apart.
+static size_t span(long long rows, long long stride, long long width, size_t es) {
+    return rows < 1 ? 0 : ((size_t)(rows - 1) * stride + width) * es;
+}
+
+static bool valid_8bit(int t) { return t == DL_I8 || t == DL_E4M3; }
+
+static dl_status rows_checks(long long rows, int width, int group, bool scaled) {
+    if (rows < 0) return fail(DL_ERR_INVALID_ARG, "rows=%lld is negative", rows);
+    if (width < 1) return fail(DL_ERR_INVALID_ARG, "width=%d must be >= 1", width);
+    if (width > 32768) return fail(DL_ERR_UNSUPPORTED, "width=%d exceeds 32768", width);
+    if (rows > 0x7fffffffLL) return fail(DL_ERR_UNSUPPORTED, "rows=%lld exceeds 2^31 - 1", rows);
+    if (rows * width > (1LL << 38)) return fail(DL_ERR_UNSUPPORTED, "rows * width exceeds 2^38");
+    if (scaled && group != 0 && group != 128) return fail(DL_ERR_UNSUPPORTED, "group=%d not in {0, 128}", group);
+    return DL_OK;
+}
+
+static size_t scale_bytes(long long rows, int width, int group) {
+    return (size_t)rows * (group ? (width + group - 1) / group : 1) * sizeof(float);
+}
+
+dl_status dl_rms_norm(const void *x, dl_dtype x_dtype, long long x_stride, const void *residual, void *residual_out,
+                      dl_dtype r_dtype, const void *weight, dl_dtype w_dtype, float eps, void *y, dl_dtype y_dtype,
+                      float *scale, int group, long long rows, int width, cudaStream_t stream) {
+    const bool scaled = valid_8bit(y_dtype), res = residual != nullptr;
+    if (!valid_dtype(x_dtype)) return fail(DL_ERR_INVALID_ARG, "unknown x dtype %d", (int)x_dtype);
+    if (!valid_dtype(w_dtype)) return fail(DL_ERR_INVALID_ARG, "unknown weight dtype %d", (int)w_dtype);
+    if (res && !valid_dtype(r_dtype)) return fail(DL_ERR_INVALID_ARG, "unknown residual dtype %d", (int)r_dtype);
+    if (!valid_dtype(y_dtype) && !scaled) return fail(DL_ERR_INVALID_ARG, "unknown y dtype %d", (int)y_dtype);
+    dl_status s = rows_checks(rows, width, group, scaled);
+    if (s != DL_OK) return s;
+    if (!(eps >= 0.f)) return fail(DL_ERR_INVALID_ARG, "eps=%g must be >= 0", (double)eps);
+    if (x_stride < width) return fail(DL_ERR_INVALID_ARG, "x_stride=%lld is less than width=%d", x_stride, width);
+    if (!res && residual_out) return fail(DL_ERR_INVALID_ARG, "residual_out without a residual");
+    if (!scaled && scale) return fail(DL_ERR_INVALID_ARG, "scale without an 8-bit y");
+    if (rows == 0) return ok();
+    const size_t xs = elem_size(x_dtype), rs = elem_size(r_dtype), ws = elem_size(w_dtype), ys = elem_size(y_dtype);
+    const size_t n = (size_t)rows * width;
+    const Buf b[6] = {{"x", x, span(rows, x_stride, width, xs), xs},
+                      {"residual", residual, n * rs, rs, !res},
+                      {"residual_out", residual_out, n * rs, rs, !res},
+                      {"weight", weight, width * ws, ws},
+                      {"y", y, n * ys, ys},
+                      {"scale", scale, scale_bytes(rows, width, group), 4, !scaled}};
+    if ((s = check_bufs(b, 6)) != DL_OK) return s;
+    // residual_out may be residual itself, element for element
+    Buf others[6] = {b[0], b[1], b[2], b[3], b[4], b[5]};
+    if (res && residual_out == residual) others[1].unused = true;
+    const Buf writers[3] = {others[2], others[4], others[5]};
+    if ((s = check_overlap(writers, 3, others, 6)) != DL_OK) return s;
+    dl::NormParams p{x,   x_stride, residual, residual_out, weight,  y,       scale,  eps,
+                     rows, width,   scaled ? group : 0, x_dtype, r_dtype, w_dtype, y_dtype};
+    return cuda_status(dl::launch_rms_norm(p, stream), "rms-norm launch");
+}
+
+dl_status dl_rows_from_8bit(const void *codes, dl_dtype c_dtype, const float *scale, int group, void *out,
+                            dl_dtype out_dtype, long long rows, int width, cudaStream_t stream) {
+    if (!valid_8bit(c_dtype)) return fail(DL_ERR_INVALID_ARG, "codes are DL_I8 or DL_E4M3 (got %d)", (int)c_dtype);
+    if (!valid_dtype(out_dtype)) return fail(DL_ERR_INVALID_ARG, "unknown out dtype %d", (int)out_dtype);
+    dl_status s = rows_checks(rows, width, group, true);
+    if (s != DL_OK) return s;
+    if (rows == 0) return ok();
+    const size_t n = (size_t)rows * width, os = elem_size(out_dtype);
+    const Buf b[3] = {{"codes", codes, n, 1}, {"scale", scale, scale_bytes(rows, width, group), 4}, {"out", out, n * os, os}};
+    if ((s = check_bufs(b, 3)) != DL_OK) return s;
+    if ((s = check_overlap(b + 2, 1, b, 3)) != DL_OK) return s;
+    return cuda_status(dl::launch_rows_from_8bit(codes, c_dtype, scale, group, out, out_dtype, rows, width, stream),
+                       "8-bit rows launch");
+}
+
+// Sequences and slots of a call: its index arrays into b (3 entries).
+static dl_status seq_checks(const int *seq_start, bool ragged, int n_seq, int T, int P, const int *slot, int *status,
+                            Buf *b) {
+    if (n_seq < 1) return fail(DL_ERR_INVALID_ARG, "the number of sequences (%d) must be >= 1", n_seq);
+    if (P < n_seq) return fail(DL_ERR_INVALID_ARG, "%d sequences need distinct slots but P=%d", n_seq, P);
+    if (T < 0) return fail(DL_ERR_INVALID_ARG, "T=%d is negative", T);
+    b[0] = {"seq_start", seq_start, (size_t)(n_seq + 1) * sizeof(int), 4, !ragged};
+    b[1] = {"slot", slot, (size_t)n_seq * sizeof(int), 4, slot == nullptr};
+    b[2] = {"status", status, sizeof(int), 4, status == nullptr};
+    return DL_OK;
+}
+
+static dl_status conv(const dl_conv *cv, const void *x, long long x_stride, int T, const int *seq_start, bool ragged,
+                      int n_seq, void *state, int P, const int *slot, int *status, void *y, cudaStream_t stream) {
+    if (!cv) return fail(DL_ERR_INVALID_ARG, "conv is a null pointer");
+    if (!valid_dtype(cv->dtype)) return fail(DL_ERR_INVALID_ARG, "unknown conv dtype %d", (int)cv->dtype);
+    if (cv->taps < 2 || cv->taps > 4) return fail(DL_ERR_UNSUPPORTED, "taps=%d not in 2..4", cv->taps);
+    if (cv->channels < 1) return fail(DL_ERR_INVALID_ARG, "channels=%d must be >= 1", cv->channels);
+    if (x_stride < cv->channels)
+        return fail(DL_ERR_INVALID_ARG, "x_stride=%lld is less than channels=%d", x_stride, cv->channels);
+    Buf b[8];
+    dl_status s = seq_checks(seq_start, ragged, n_seq, T, P, slot, status, b);
+    if (s != DL_OK) return s;
+    if (((long long)T / 32 + n_seq) * cv->channels > (1LL << 38))
+        return fail(DL_ERR_UNSUPPORTED, "T * channels exceeds the launch limit");
+    if (T == 0) return ok();
+    const size_t es = elem_size(cv->dtype), C = cv->channels;
+    b[3] = {"conv.w", cv->w, C * cv->taps * es, es};
+    b[4] = {"conv.bias", cv->bias, C * es, es, cv->bias == nullptr};
+    b[5] = {"x", x, span(T, x_stride, C, es), es};
+    b[6] = {"state", state, (size_t)P * (cv->taps - 1) * C * es, es};
+    b[7] = {"y", y, (size_t)T * C * es, es};
+    if ((s = check_bufs(b, 8)) != DL_OK) return s;
+    const Buf writers[3] = {b[2], b[6], b[7]};
+    if ((s = check_overlap(writers, 3, b, 8)) != DL_OK) return s;
+    dl::ConvParams p{cv->w, cv->bias, x, x_stride, state, y, cv->channels, cv->taps, cv->dtype, cv->silu != 0};
+    dl::SeqIdx q{seq_start, slot, status, n_seq, T, P};
+    return cuda_status(ragged ? dl::launch_conv_prompt(p, q, stream) : dl::launch_conv_step(p, q, stream),
+                       "convolution launch");
+}
+
+dl_status dl_conv_prompt(const dl_conv *cv, const void *x, long long x_stride, int T, const int *seq_start, int n_seq,
+                         void *state, int P, const int *slot, int *status, void *y, cudaStream_t stream) {
+    return conv(cv, x, x_stride, T, seq_start, true, n_seq, state, P, slot, status, y, stream);
+}
+
+dl_status dl_conv_step(const dl_conv *cv, const void *x, long long x_stride, int B, void *state, int P,
+                       const int *slot, int *status, void *y, cudaStream_t stream) {
+    return conv(cv, x, x_stride, B, nullptr, false, B, state, P, slot, status, y, stream);
+}
+
+static dl_status ssm_checks(const dl_ssm *in, void *S, dl_dtype s_dt, int P, const int *slot, int *status,
+                            const int *seq_start, bool ragged, int n_seq, int T, void *y, int H, int G, int dk, int dv,
+                            Buf *b, int &nb) {
+    if (!in) return fail(DL_ERR_INVALID_ARG, "in is a null pointer");
+    dl_status s = seq_checks(seq_start, ragged, n_seq, T, P, slot, status, b);
+    if (s != DL_OK) return s;
+    if (H < 1) return fail(DL_ERR_INVALID_ARG, "H=%d must be >= 1", H);
+    if ((s = check_dims(P, H, dk, dv, s_dt, in->dtype)) != DL_OK) return s;
+    if (s_dt == DL_I8) return fail(DL_ERR_UNSUPPORTED, "the scan takes a float32 or bfloat16 state");
+    if (G < 1 || H % G) return fail(DL_ERR_INVALID_ARG, "G=%d does not divide H=%d", G, H);
+    const size_t es = elem_size(in->dtype);
+    const struct {
+        const char *name;
+        const void *p;
+        long long stride, width;
+        bool vec, optional;
+    } rows[5] = {{"x", in->x, in->x_stride, (long long)H * dv, true, false},
+                 {"dt", in->dt, in->dt_stride, H, false, false},
+                 {"b", in->b, in->b_stride, (long long)G * dk, true, false},
+                 {"c", in->c, in->c_stride, (long long)G * dk, true, false},
+                 {"z", in->z, in->z_stride, (long long)H * dv, true, true}};
+    nb = 3;
+    for (const auto &r : rows) {
+        const bool unused = r.optional && !r.p;
+        if (!unused && r.stride < r.width)
+            return fail(DL_ERR_INVALID_ARG, "%s_stride=%lld is less than its row of %lld", r.name, r.stride, r.width);
+        if (!unused && r.vec && (unsigned long long)r.stride * es % 16)
+            return fail(DL_ERR_INVALID_ARG, "%s_stride=%lld is not a multiple of 16 bytes", r.name, r.stride);
+        b[nb++] = {r.name, r.p, span(T, r.stride, r.width, es), r.vec ? 16 : es, unused};
+    }
+    b[nb++] = {"A", in->A, (size_t)H * sizeof(float), 4};
+    b[nb++] = {"D", in->D, (size_t)H * sizeof(float), 4, in->D == nullptr};
+    b[nb++] = {"dt_bias", in->dt_bias, (size_t)H * sizeof(float), 4, in->dt_bias == nullptr};
+    b[nb++] = {"S", S, state_bytes(s_dt, (size_t)P * H, dk, dv), 16};
+    b[nb++] = {"y", y, (size_t)T * H * dv * es, 16};
+    return DL_OK;
+}
+
+size_t dl_ssm_work_bytes(int T, int n_seq, int H, int d_k, int d_v) {
+    if (T < 0 || n_seq < 1 || H < 1 || d_k < 1 || d_v < 1) return 0;
+    return dl::ssm_work_bytes(T, n_seq, H, d_k, d_v);
+}
+
+dl_status dl_ssm_prompt(void *S, dl_dtype s_dtype, int P, const int *slot, int *status, const dl_ssm *in,
+                        const int *seq_start, int n_seq, int T, void *y, int H, int G, int d_k, int d_v, void *work,
+                        size_t work_bytes, cudaStream_t stream) {
+    Buf b[14];
+    int nb = 0;
+    dl_status s = ssm_checks(in, S, s_dtype, P, slot, status, seq_start, true, n_seq, T, y, H, G, d_k, d_v, b, nb);
+    if (s != DL_OK) return s;
+    if (T == 0) return ok();
+    if ((long long)n_seq * H * d_v > (1LL << 34)) return fail(DL_ERR_UNSUPPORTED, "n_seq * H * d_v exceeds 2^34");
+    const size_t need = dl::ssm_work_bytes(T, n_seq, H, d_k, d_v);
+    b[nb++] = {"work", work, need, 16, need == 0};
+    if ((s = check_bufs(b, nb)) != DL_OK) return s;
+    if (work_bytes < need) return fail(DL_ERR_INVALID_ARG, "work holds %zu bytes, needs %zu", work_bytes, need);
+    const Buf writers[4] = {b[2], b[11], b[12], b[13]};
+    if ((s = check_overlap(writers, 4, b, nb)) != DL_OK) return s;
+    dl::SsmParams p{*in, S, y, H, G, d_k, d_v, s_dtype};
+    dl::SeqIdx q{seq_start, slot, status, n_seq, T, P};
+    return cuda_status(dl::launch_ssm_prompt(p, q, work, stream), "scan launch");
+}
+
+dl_status dl_ssm_step(void *S, dl_dtype s_dtype, int P, const int *slot, int *status, const dl_ssm *in, void *y,
+                      int B, int H, int G, int d_k, int d_v, cudaStream_t stream) {
+    Buf b[13];
+    int nb = 0;
+    dl_status s = ssm_checks(in, S, s_dtype, P, slot, status, nullptr, false, B, B, y, H, G, d_k, d_v, b, nb);
+    if (s != DL_OK) return s;
+    if ((s = check_bufs(b, nb)) != DL_OK) return s;
+    const Buf writers[3] = {b[2], b[11], b[12]};
+    if ((s = check_overlap(writers, 3, b, nb)) != DL_OK) return s;
+    dl::SsmParams p{*in, S, y, H, G, d_k, d_v, s_dtype};
+    dl::SeqIdx q{nullptr, slot, status, B, B, P};
+    return cuda_status(dl::launch_ssm_step(p, q, stream), "scan step launch");
 }
 
 const char *dl_status_string(dl_status s) {

@@ -1,0 +1,213 @@
+// Short causal convolution along the tokens, for ragged prompts and for single
+// tokens, with each slot's last taps - 1 inputs as its state.
+//
+//   y_t[c] = act(bias[c] + sum_{j < K} w[c, j] x_{t-K+1+j}[c])
+//
+// HBM-bound (2 K + 5 operations per element moved twice): every input and
+// output moves once. A thread owns 16 bytes of channels and walks TT tokens
+// with the K - 1 inputs before them in registers, so an input is loaded once
+// and used K times; the loads of 8 tokens are issued before the first is used.
+// A prompt's first tile reads its slot's history and also writes the new one
+// (the last K - 1 inputs, from x): no other thread reads that history, so the
+// update needs no second launch.
+#include "launch.h"
+
+namespace dl {
+
+namespace {
+
+// VEC elements as loaded (VEC = 1: any alignment; else 16 bytes).
+template <class T, int VEC>
+struct Raw {
+    T v[VEC];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VEC == 1)
+            v[0] = *p;
+        else
+            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (VEC == 1)
+            *p = v[0];
+        else
+            *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(v);
+    }
+};
+template <class T, int VEC>
+struct alignas(16) RawV : Raw<T, VEC> {};
+
+template <class T, int K, int VEC>
+struct Filter {
+    float w[VEC][K], bias[VEC];
+    __device__ __forceinline__ void load(const ConvParams &p, int ch) {
+        const T *wp = static_cast<const T *>(p.w) + (long long)ch * K;
+        if constexpr (VEC == 1) {
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[0][j] = to_f(wp[j]);
+        } else {  // VEC K elements: K times 16 bytes
+            float f[VEC * K];
+            load_vec<VEC * K>(wp, f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+#pragma unroll
+                for (int j = 0; j < K; ++j) w[e][j] = f[e * K + j];
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) bias[e] = p.bias ? to_f(static_cast<const T *>(p.bias)[ch + e]) : 0.f;
+    }
+};
+
+template <class T, int K, int VEC, int TT>
+__global__ void __launch_bounds__(256) conv_prompt_kernel(const ConvParams p, const SeqIdx q, int nv) {
+    using R = RawV<T, VEC>;
+    constexpr int U = 8;  // tokens whose loads are in flight
+    static_assert(TT % U == 0 && TT >= K, "tile");
+    const long long gid = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (gid < q.n_seq) seq_check(q, (int)gid);
+    const long long tile = gid / nv;
+    if (tile >= (long long)q.T / TT + q.n_seq) return;
+    const int ch = (int)(gid - tile * nv) * VEC;
+    int in_seq = 0, s0, n;
+    const int i = seq_of_tile(q, (int)tile, TT, in_seq);
+    if (i < 0 || !seq_range(q, i, s0, n)) return;
+    const int slot = seq_slot(q, i);
+    if (slot < 0 || in_seq >= (n + TT - 1) / TT) return;
+    const int t0 = in_seq * TT, t1 = min(t0 + TT, n), C = p.channels;
+    const T *x = static_cast<const T *>(p.x) + (long long)s0 * p.x_stride + ch;
+    T *y = static_cast<T *>(p.y) + (long long)s0 * C + ch;
+    Filter<T, K, VEC> f;
+    R hist[K - 1];
+    if (t0 == 0) {
+        T *st = static_cast<T *>(p.state) + (long long)slot * (K - 1) * C + ch;
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) hist[j].load(st + (long long)j * C);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {  // the slot's new history
+            const int pos = n - (K - 1) + j;
+            R r;
+            if (pos >= 0) {
+                r.load(x + (long long)pos * p.x_stride);
+            } else {  // hist[pos + K - 1], by constant indices
+#pragma unroll
+                for (int m = 0; m < K - 1; ++m)
+                    if (m == pos + K - 1) r = hist[m];
+            }
+            r.store(st + (long long)j * C);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) hist[j].load(x + (long long)(t0 - (K - 1) + j) * p.x_stride);
+    }
+    f.load(p, ch);
+    float win[K - 1 + U][VEC];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) win[j][e] = to_f(hist[j].v[e]);
+    for (int t = t0; t < t1; t += U) {
+        R raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < t1) raw[u].load(x + (long long)(t + u) * p.x_stride);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + u < t1) {
+                R out;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    win[K - 1 + u][e] = to_f(raw[u].v[e]);
+                    float acc = f.bias[e];
+#pragma unroll
+                    for (int j = 0; j < K; ++j) acc = fmaf(f.w[e][j], win[u + j][e], acc);
+                    store_f(&out.v[e], p.silu ? silu_f<T>(acc) : acc);
+                }
+                out.store(y + (long long)(t + u) * C);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) win[j][e] = win[U + j][e];
+    }
+}
+
+template <class T, int K, int VEC>
+__global__ void __launch_bounds__(256) conv_step_kernel(const ConvParams p, const SeqIdx q, int nv) {
+    using R = RawV<T, VEC>;
+    const long long gid = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (gid < q.n_seq) seq_check(q, (int)gid);
+    const long long row = gid / nv;
+    if (row >= q.n_seq) return;
+    const int ch = (int)(gid - row * nv) * VEC, C = p.channels;
+    const int slot = seq_slot(q, (int)row);
+    if (slot < 0) return;
+    T *st = static_cast<T *>(p.state) + (long long)slot * (K - 1) * C + ch;
+    R in[K];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) in[j].load(st + (long long)j * C);
+    in[K - 1].load(static_cast<const T *>(p.x) + row * p.x_stride + ch);
+    Filter<T, K, VEC> f;
+    f.load(p, ch);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) in[j + 1].store(st + (long long)j * C);
+    R out;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        float acc = f.bias[e];
+#pragma unroll
+        for (int j = 0; j < K; ++j) acc = fmaf(f.w[e][j], to_f(in[j].v[e]), acc);
+        store_f(&out.v[e], p.silu ? silu_f<T>(acc) : acc);
+    }
+    out.store(static_cast<T *>(p.y) + row * C + ch);
+}
+
+constexpr int TT = 32;  // tokens a thread walks
+
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// f(T{}, K constant, VEC constant): VEC fills 16 bytes where every row, the
+// filter and the histories allow it, else 1.
+template <class F>
+cudaError_t dispatch_conv(const ConvParams &p, F &&f) {
+    auto with_k = [&](auto t, auto vec) -> cudaError_t {
+        switch (p.taps) {
+            case 2: return f(t, std::integral_constant<int, 2>{}, vec);
+            case 3: return f(t, std::integral_constant<int, 3>{}, vec);
+            case 4: return f(t, std::integral_constant<int, 4>{}, vec);
+        }
+        return cudaErrorInvalidValue;
+    };
+    auto with_t = [&](auto t) -> cudaError_t {
+        constexpr int V = 16 / (int)sizeof(t);
+        const bool wide = p.channels % V == 0 && p.x_stride % V == 0 && aligned16(p.x) && aligned16(p.y) &&
+                          aligned16(p.state) && aligned16(p.w);
+        return wide ? with_k(t, std::integral_constant<int, V>{}) : with_k(t, std::integral_constant<int, 1>{});
+    };
+    return p.dt == DL_BF16 ? with_t(bf16{}) : with_t(float{});
+}
+
+}  // namespace
+
+cudaError_t launch_conv_prompt(const ConvParams &p, const SeqIdx &q, cudaStream_t st) {
+    return dispatch_conv(p, [&](auto t, auto k, auto vec) -> cudaError_t {
+        using T = decltype(t);
+        constexpr int K = decltype(k)::value, V = decltype(vec)::value;
+        const int nv = p.channels / V;
+        const long long threads = ((long long)q.T / TT + q.n_seq) * nv;
+        conv_prompt_kernel<T, K, V, TT><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(p, q, nv);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_conv_step(const ConvParams &p, const SeqIdx &q, cudaStream_t st) {
+    return dispatch_conv(p, [&](auto t, auto k, auto vec) -> cudaError_t {
+        using T = decltype(t);
+        constexpr int K = decltype(k)::value, V = decltype(vec)::value;
+        const int nv = p.channels / V;
+        const long long threads = (long long)q.n_seq * nv;
+        conv_step_kernel<T, K, V><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(p, q, nv);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace dl

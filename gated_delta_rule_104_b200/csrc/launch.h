@@ -10,6 +10,7 @@
 
 #include "../../include/deltalog.h"
 #include "common.cuh"
+#include "seq_index.h"
 
 namespace dl {
 
@@ -120,6 +121,66 @@ cudaError_t read_guard_merge_tc(unsigned int *flags, unsigned int *line, bool cl
 // State conversions to / from the int8 layout (rows = B*H*d_v rows of d_k).
 cudaError_t launch_to_i8(const void *S, dl_dtype s_dt, void *S_i8, long long rows, int dk, cudaStream_t st);
 cudaError_t launch_from_i8(const void *S_i8, void *S, dl_dtype s_dt, long long rows, int dk, cudaStream_t st);
+
+// ---- norm, short convolution, selective scan (norm.cu, conv.cu, ssm.cu)
+
+struct NormParams {
+    const void *x;
+    long long x_stride;
+    const void *res;  // null: no residual
+    void *res_out;
+    const void *w;
+    void *y;
+    float *scale;  // 8-bit outputs
+    float eps;
+    long long rows;
+    int width, group;
+    dl_dtype x_dt, r_dt, w_dt, y_dt;
+};
+cudaError_t launch_rms_norm(const NormParams &p, cudaStream_t st);
+cudaError_t launch_rows_from_8bit(const void *codes, dl_dtype c_dt, const float *scale, int group, void *out,
+                                  dl_dtype out_dt, long long rows, int width, cudaStream_t st);
+
+// Flags a bad sequence or slot; called once for each i of a call.
+__device__ __forceinline__ void seq_check(const SeqIdx &q, int i) {
+    if (!q.status) return;
+    int s0, n, bad = seq_slot(q, i) < 0 ? 1 : 0;
+    if (q.seq_start && !seq_range(q, i, s0, n)) bad |= 2;
+    if (bad) atomicOr(q.status, bad);
+}
+
+struct ConvParams {
+    const void *w, *bias;  // bias may be null
+    const void *x;
+    long long x_stride;
+    void *state, *y;
+    int channels, taps;
+    dl_dtype dt;
+    bool silu;
+};
+cudaError_t launch_conv_prompt(const ConvParams &p, const SeqIdx &q, cudaStream_t st);
+cudaError_t launch_conv_step(const ConvParams &p, const SeqIdx &q, cudaStream_t st);
+
+struct SsmParams {
+    dl_ssm in;
+    void *S, *y;
+    int H, G, dk, dv;
+    dl_dtype s_dt;
+};
+cudaError_t launch_ssm_prompt(const SsmParams &p, const SeqIdx &q, void *work, cudaStream_t st);
+cudaError_t launch_ssm_step(const SsmParams &p, const SeqIdx &q, cudaStream_t st);
+size_t ssm_work_bytes(int T, int n_seq, int H, int dk, int dv);
+
+// u / (1 + exp(-u)): the fast exponential and division where the result is
+// rounded to bf16, the accurate ones otherwise.
+template <class T>
+__device__ __forceinline__ float silu_f(float u) {
+    if constexpr (sizeof(T) == 2) return __fdividef(u, 1.f + __expf(-u));
+    return u / (1.f + expf(-u));
+}
+__device__ __forceinline__ float softplus_f(float u) { return fmaxf(u, 0.f) + log1pf(expf(-fabsf(u))); }
+__device__ __forceinline__ void store_f(float *p, float x) { *p = x; }
+__device__ __forceinline__ void store_f(bf16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
 // Pool bookkeeping after a step (advance = true: count + 1, or 0 after the L-th
 // entry merged) or a flush (advance = false: count = 0), for each batch row's slot.

@@ -1,0 +1,61 @@
+// Index arithmetic of calls over ragged sequences and pool slots. Host-callable,
+// so that the CPU tests replay what the kernels compute.
+#pragma once
+
+#ifndef DL_HD
+#ifdef __CUDACC__
+#define DL_HD __host__ __device__
+#else
+#define DL_HD
+#endif
+#endif
+
+namespace dl {
+
+// Which rows a call works on: sequences seq_start[i] .. seq_start[i + 1] of T
+// rows (prompts), or row i alone (seq_start == nullptr: one token each), and
+// the pool slot of each (slot == nullptr: slot i).
+struct SeqIdx {
+    const int *seq_start;
+    const int *slot;
+    int *status;
+    int n_seq, T, P;
+};
+
+// Slot of sequence i, or -1.
+DL_HD inline int seq_slot(const SeqIdx &q, int i) {
+    const int s = q.slot ? q.slot[i] : i;
+    return s >= 0 && s < q.P ? s : -1;
+}
+// First row and length of sequence i; false (and n = 0) if its bounds are bad.
+DL_HD inline bool seq_range(const SeqIdx &q, int i, int &s0, int &n) {
+    s0 = q.seq_start[i];
+    const int s1 = q.seq_start[i + 1];
+    const bool good = s0 >= 0 && s0 <= s1 && s1 <= q.T;
+    n = good ? s1 - s0 : 0;
+    return good;
+}
+// Ragged sequences cut into tiles of `len` rows, each from its own start, as
+// one grid: sequence i takes tile numbers from seq_start[i] / len + i on. The
+// next sequence's first number is at least ceil(n / len) further, so numbers
+// never collide, and n_seq + T / len of them cover every sequence without the
+// host knowing the lengths. Finds the sequence of a tile number and the tile
+// in it; -1 for none.
+DL_HD inline int seq_tile_base(const SeqIdx &q, int i, int len) {
+    const int s = q.seq_start[i];
+    return (s > 0 ? s : 0) / len + i;
+}
+DL_HD inline int seq_of_tile(const SeqIdx &q, int tile, int len, int &in_seq) {
+    int lo = -1, hi = q.n_seq - 1;
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (seq_tile_base(q, mid, len) <= tile)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    if (lo >= 0) in_seq = tile - seq_tile_base(q, lo, len);
+    return lo;
+}
+
+}  // namespace dl

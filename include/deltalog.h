@@ -62,7 +62,7 @@
 extern "C" {
 #endif
 
-#define DL_ABI_VERSION 9
+#define DL_ABI_VERSION 10
 #define DL_MAX_LOG 64
 
 typedef enum {
@@ -84,8 +84,10 @@ typedef enum {
  * correctly rounded fp32 operation on the row's fp32 values. (The low-precision base of the DAMP
  * abstract, "Decay-Aware Mixed-Precision Recurrent-State Quantization": with
  * the deferred schedule the base is rounded once per merge, not every step.)
- * The eager steps take DL_F32 or DL_BF16 only (DL_I8 -> DL_ERR_UNSUPPORTED). */
-typedef enum { DL_F32 = 0, DL_BF16 = 1, DL_I8 = 2 } dl_dtype;
+ * The eager steps take DL_F32 or DL_BF16 only (DL_I8 -> DL_ERR_UNSUPPORTED).
+ * DL_E4M3 (8-bit floating point, 4 exponent and 3 mantissa bits, largest value
+ * 448) is an output type of dl_rms_norm only; DL_I8 is one too. */
+typedef enum { DL_F32 = 0, DL_BF16 = 1, DL_I8 = 2, DL_E4M3 = 3 } dl_dtype;
 
 /* The model's update rule: its decay shape and whether the delta-rule
  * correction applies. */
@@ -308,6 +310,150 @@ dl_status dl_state_to_i8(const void *S, dl_dtype s_dtype, void *S_i8,
  * DL_BF16, rounded to nearest-even for DL_BF16). */
 dl_status dl_state_from_i8(const void *S_i8, void *S, dl_dtype s_dtype,
                            int B, int H, int d_k, int d_v, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Operators around a recurrent layer's step: the norm in front of its
+ * projections (and behind its output), the short causal convolution of its
+ * inputs, and the selective state space scan, whose state has the layout of
+ * the steps above. Each has a form for prompts (ragged sequences laid end to
+ * end) and one for single tokens; sequences own slots of caller-owned pools of
+ * states, as in dl_pool. No page of the sources describes them.
+ *
+ * Common to them
+ *   Rows       "stride" is a row stride in elements, at least the row's
+ *              width; inside a row the elements are contiguous. An operand
+ *              given without a stride is contiguous.
+ *   Sequences  seq_start [n_seq + 1] int32, device: sequence i holds token rows
+ *              seq_start[i] .. seq_start[i+1]-1 of the T rows. Ascending; empty
+ *              sequences are allowed (their slot stays as it is). Rows before
+ *              the first and behind the last sequence are neither read nor
+ *              written. A sequence with bounds outside [0, T] or descending
+ *              ORs 2 into *status and is skipped (what the call then computes
+ *              for the others is unspecified, but it stays inside the arrays).
+ *   Slots      slot [n_seq] or [B] int32, device, or null (sequence i owns slot
+ *              i): the slots of one call must be distinct. A row whose slot is
+ *              outside [0, P) is skipped (no output, no state written) and ORs
+ *              1 into *status (status may be null), so a batch padded for a
+ *              captured graph names slot -1 in its padding rows.
+ *   Stream     one call's results do not depend on other calls' work unless
+ *              they share a slot or a workspace; such calls must be ordered by
+ *              the caller. Every sum has a fixed order: the same call gives the
+ *              same bits.
+ */
+
+/* Root-mean-square norm of rows, with the residual's addition:
+ *   h = x (+ residual, then residual_out = h),
+ *   y = h / sqrt(mean(h^2) + eps) * weight,
+ * in fp32 from the unrounded h; each output is rounded once.
+ *   x        [rows, width] x_dtype (DL_F32 or DL_BF16), row stride x_stride
+ *   residual [rows, width] r_dtype (DL_F32 or DL_BF16), or null for none (then
+ *            residual_out is null too); residual_out may be residual itself,
+ *            and may overlap no other operand
+ *   weight   [width] w_dtype (DL_F32 or DL_BF16)
+ *   y        [rows, width] y_dtype: DL_F32, DL_BF16, or 8 bits with scales:
+ *            DL_I8 (scale = max|y| / 127, code = the nearest integer to
+ *            y / scale, ties to even) or DL_E4M3 (scale = max|y| / 448, code =
+ *            y / scale rounded to nearest even)
+ *   group    8-bit outputs: columns per scale, 128, or 0 for one scale a row
+ *   scale    8-bit outputs: [rows, ceil(width / group)] (or [rows]) float;
+ *            otherwise null. A group of zeros has scale 0; a group that holds
+ *            a NaN or an infinity has scale NaN.
+ * rows >= 0 (0: nothing to do), width 1..32768. Pointers need only their
+ * element's alignment; 16-byte aligned rows of a multiple of 8 elements take
+ * the wide path. */
+dl_status dl_rms_norm(const void *x, dl_dtype x_dtype, long long x_stride,
+                      const void *residual, void *residual_out, dl_dtype r_dtype,
+                      const void *weight, dl_dtype w_dtype, float eps,
+                      void *y, dl_dtype y_dtype, float *scale, int group,
+                      long long rows, int width, cudaStream_t stream);
+
+/* The values of dl_rms_norm's 8-bit rows (code * scale) as out_dtype (DL_F32
+ * or DL_BF16): codes [rows, width] c_dtype (DL_I8 or DL_E4M3), scale and group
+ * as there, out [rows, width]. */
+dl_status dl_rows_from_8bit(const void *codes, dl_dtype c_dtype, const float *scale, int group,
+                            void *out, dl_dtype out_dtype, long long rows, int width,
+                            cudaStream_t stream);
+
+/* A short causal convolution along the tokens, one filter per channel:
+ *   y_t[c] = act(bias[c] + sum_{j < taps} w[c, j] x_{t - taps + 1 + j}[c]),
+ * act(u) = u / (1 + exp(-u)) if silu, else u; sums in fp32. The inputs before a
+ * sequence's first token come from its slot's history.
+ *   w [channels, taps], bias [channels] or null; taps in 2..4 */
+typedef struct {
+    const void *w;
+    const void *bias;
+    int channels;
+    int taps;
+    dl_dtype dtype; /* DL_F32 or DL_BF16: w, bias, x, the histories and y */
+    int silu;
+} dl_conv;
+
+/* The convolution over prompts.
+ *   x       [T, channels], row stride x_stride
+ *   state   [P, taps - 1, channels]: each slot's last inputs, oldest first;
+ *           read as the tokens before the sequence and replaced by its own last
+ *           taps - 1 (zeros for a new sequence)
+ *   y       [T, channels]
+ * T >= 0 and n_seq >= 1. Pointers need only their element's alignment; 16-byte
+ * aligned rows of a multiple of 16 bytes take the wide path. */
+dl_status dl_conv_prompt(const dl_conv *conv, const void *x, long long x_stride, int T,
+                         const int *seq_start, int n_seq,
+                         void *state, int P, const int *slot, int *status,
+                         void *y, cudaStream_t stream);
+
+/* The convolution of one new token for each of B sequences: x [B, channels]
+ * (row stride x_stride), y [B, channels]; state as above. */
+dl_status dl_conv_step(const dl_conv *conv, const void *x, long long x_stride, int B,
+                       void *state, int P, const int *slot, int *status,
+                       void *y, cudaStream_t stream);
+
+/* Inputs of the selective state space scan. Per token and head h of group
+ * g = h / (H / G),
+ *   dt = softplus(dt_raw + dt_bias[h]),
+ *   S <- exp(dt A[h]) S + dt x b_g^T,    y = S c_g + D[h] x  (times z / (1 + exp(-z)))
+ * with S in R^{d_v x d_k}, x, y, z in R^{d_v}, b, c in R^{d_k}: the head-wise decay
+ * of the steps above with k = b, q = c, v = dt x and no delta correction.
+ * Vector rows (x, b, c, z) must start at 16-byte boundaries (pointer and row
+ * stride); dt needs only its element's alignment. A must be <= 0. */
+typedef struct {
+    const void *x;        /* [rows, H, d_v], row stride x_stride */
+    long long x_stride;
+    const void *dt;       /* [rows, H] */
+    long long dt_stride;
+    const void *b;        /* [rows, G, d_k] */
+    long long b_stride;
+    const void *c;        /* [rows, G, d_k] */
+    long long c_stride;
+    const void *z;        /* [rows, H, d_v] or null (no gate) */
+    long long z_stride;
+    const float *A;       /* [H] */
+    const float *D;       /* [H] or null (0) */
+    const float *dt_bias; /* [H] or null (0) */
+    dl_dtype dtype;       /* DL_F32 or DL_BF16: x, dt, b, c, z and y */
+} dl_ssm;
+
+/* Bytes of workspace dl_ssm_prompt needs (0 if none) for T token rows in n_seq
+ * sequences; 0 for a bad argument. */
+size_t dl_ssm_work_bytes(int T, int n_seq, int H, int d_k, int d_v);
+
+/* The scan over prompts: every sequence starts from its slot's state and
+ * leaves its last state there (a chunk of a longer prompt continues it).
+ *   S    [P, H, d_v, d_k] s_dtype (DL_F32 or DL_BF16; a bf16 state is advanced in
+ *        fp32 and rounded once at the sequence's end)
+ *   y    [T, H, d_v] in->dtype
+ *   work dl_ssm_work_bytes(...) bytes, 16-byte aligned (null if that is 0),
+ *        contents irrelevant between calls
+ * T >= 0, n_seq >= 1, G divides H. */
+dl_status dl_ssm_prompt(void *S, dl_dtype s_dtype, int P, const int *slot, int *status,
+                        const dl_ssm *in, const int *seq_start, int n_seq, int T,
+                        void *y, int H, int G, int d_k, int d_v,
+                        void *work, size_t work_bytes, cudaStream_t stream);
+
+/* The scan of one new token for each of B sequences (x, dt, b, c, z, y of B
+ * rows); S as above, rounded after the step. */
+dl_status dl_ssm_step(void *S, dl_dtype s_dtype, int P, const int *slot, int *status,
+                      const dl_ssm *in, void *y, int B, int H, int G, int d_k, int d_v,
+                      cudaStream_t stream);
 
 /* Static text for a status code. */
 const char *dl_status_string(dl_status s);
