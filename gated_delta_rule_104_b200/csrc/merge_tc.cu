@@ -640,29 +640,11 @@ merge_tc_kernel(const __grid_constant__ CUtensorMap map_s, const __grid_constant
 
 // ---------------------------------------------------------------- host side
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
-// against the driver library); looked up once.
-EncodeTiledFn encoder() {
-    static EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
-}
-
 // The fp32 state [rows, 128] as a tensor map of box_cols x box_rows boxes
 // (box_cols x 4 bytes = the swizzle span: 32 columns with 128-byte swizzle,
 // 16 with 64-byte).
 cudaError_t state_map(CUtensorMap *m, void *S, unsigned long long rows, unsigned box_cols, unsigned box_rows) {
-    EncodeTiledFn fn = encoder();
+    tc::EncodeTiledFn fn = tc::encoder();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)DK, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)DK * 4};
@@ -679,7 +661,7 @@ cudaError_t state_map(CUtensorMap *m, void *S, unsigned long long rows, unsigned
 // The int8 codes [rows, 128] as a tensor map of 128 x 128 boxes (one unit's
 // codes; 128-byte rows under 128-byte swizzle).
 cudaError_t code_map(CUtensorMap *m, void *codes, unsigned long long rows) {
-    EncodeTiledFn fn = encoder();
+    tc::EncodeTiledFn fn = tc::encoder();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)DK, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)DK};
@@ -733,7 +715,7 @@ bool merge_tc_supported(const StepParams &p, int n_log, bool with_cur, const Poo
     const long long rows = (long long)p.B * p.H * p.dv;
     return pool.slot == nullptr && (p.s_dt == DL_F32 || p.s_dt == DL_I8) && p.dk == DK && p.dv % ROWS == 0 &&
            n_log + (with_cur ? 1 : 0) <= NB && n_log + (with_cur ? 1 : 0) >= 1 && rows < (1LL << 31) &&
-           encoder() != nullptr;
+           tc::encoder() != nullptr;
 }
 
 cudaError_t launch_merge_tc(const StepParams &p, const LogParams &lg, int n_log, bool with_cur, cudaStream_t st) {

@@ -58,4 +58,10 @@ DL_HD inline int seq_of_tile(const SeqIdx &q, int tile, int len, int &in_seq) {
     return lo;
 }
 
+// Segments of `len` rows of a sequence that has more than one: their numbers in
+// the scan's workspace start here. A sequence of n > len rows has at most
+// 2 n / len of them, so numbers never collide, and 2 T / len + 1 suffice.
+DL_HD inline int seg_base(int s0, int len) { return (int)((2LL * s0 + len - 1) / len); }
+DL_HD inline long long seg_count(int T, int len) { return 2LL * T / len + 1; }
+
 }  // namespace dl

@@ -226,6 +226,7 @@ cudaError_t launch_ssm_step(const SsmParams &p, const SeqIdx &q, cudaStream_t st
 }
 
 cudaError_t launch_ssm_prompt(const SsmParams &p, const SeqIdx &q, void *, cudaStream_t st) {
+    if (ssm_tc_supported(p)) return launch_ssm_tc(p, q, st);
     return dispatch_ssm(p, [&](auto s, auto t, auto dk) -> cudaError_t {
         using ST = decltype(s);
         using IT = decltype(t);

@@ -242,6 +242,26 @@ __host__ __device__ constexpr uint32_t swz64(uint32_t off) { return off ^ ((off 
 // 32-byte swizzling: bit 4 XOR bit 7.
 __host__ __device__ constexpr uint32_t swz32(uint32_t off) { return off ^ ((off & 0x80u) >> 3); }
 
+// ------------------------------------------------------------------ host: tensor maps
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
+// against the driver library); looked up once.
+inline EncodeTiledFn encoder() {
+    static EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
 // ------------------------------------------------------------------ TF32 split
 
 // x = hi + lo with hi = x with its low 13 mantissa bits cleared (the value a

@@ -467,7 +467,8 @@ int dl_abi_version(void);
 
 /* Fault word of the library's kernels on the current device. The kernels that
  * wait on on-chip barriers (the tcgen05 merge of dl_log_merge and
- * dl_log_merge_read, and the one-kernel form of dl_log_append_read) bound
+ * dl_log_merge_read, the one-kernel form of dl_log_append_read, and the
+ * tcgen05 scan of dl_ssm_prompt) bound
  * every such wait; a wait that runs out (about two
  * seconds; it means a bug, not a slow GPU) sets bit 0 here, abandons its work
  * (the state it was merging is then unspecified) and returns, so the device
