@@ -171,7 +171,7 @@ cudaError_t launch_ssm_prompt(const SsmParams &p, const SeqIdx &q, void *work, c
 cudaError_t launch_ssm_step(const SsmParams &p, const SeqIdx &q, cudaStream_t st);
 // The prompts' scan on the tcgen05 tensor cores (ssm_tc.cu), for bfloat16 inputs.
 bool ssm_tc_supported(const SsmParams &p);
-cudaError_t launch_ssm_tc(const SsmParams &p, const SeqIdx &q, cudaStream_t st);
+cudaError_t launch_ssm_tc(const SsmParams &p, const SeqIdx &q, void *work, cudaStream_t st);
 cudaError_t read_ssm_faults(unsigned int *out, bool clear);
 size_t ssm_work_bytes(int T, int n_seq, int H, int dk, int dv);
 

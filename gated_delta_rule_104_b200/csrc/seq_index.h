@@ -41,20 +41,23 @@ DL_HD inline bool seq_range(const SeqIdx &q, int i, int &s0, int &n) {
 // never collide, and n_seq + T / len of them cover every sequence without the
 // host knowing the lengths. Finds the sequence of a tile number and the tile
 // in it; -1 for none.
-DL_HD inline int seq_tile_base(const SeqIdx &q, int i, int len) {
+DL_HD inline int seq_tile_base(const SeqIdx &q, int i, int len, int gap) {
     const int s = q.seq_start[i];
-    return (s > 0 ? s : 0) / len + i;
+    return (s > 0 ? s : 0) / len + gap * i;
 }
-DL_HD inline int seq_of_tile(const SeqIdx &q, int tile, int len, int &in_seq) {
+// gap 1: as above. gap 0: the numbers of tiles that are not a sequence's last
+// (ceil(n / len) - 1 <= floor(n / len) of them, T / len in all): sequences of one
+// tile share a number with the next one, which the search prefers.
+DL_HD inline int seq_of_tile(const SeqIdx &q, int tile, int len, int &in_seq, int gap = 1) {
     int lo = -1, hi = q.n_seq - 1;
     while (lo < hi) {
         const int mid = lo + (hi - lo + 1) / 2;
-        if (seq_tile_base(q, mid, len) <= tile)
+        if (seq_tile_base(q, mid, len, gap) <= tile)
             lo = mid;
         else
             hi = mid - 1;
     }
-    if (lo >= 0) in_seq = tile - seq_tile_base(q, lo, len);
+    if (lo >= 0) in_seq = tile - seq_tile_base(q, lo, len, gap);
     return lo;
 }
 
@@ -63,5 +66,30 @@ DL_HD inline int seq_of_tile(const SeqIdx &q, int tile, int len, int &in_seq) {
 // 2 n / len of them, so numbers never collide, and 2 T / len + 1 suffice.
 DL_HD inline int seg_base(int s0, int len) { return (int)((2LL * s0 + len - 1) / len); }
 DL_HD inline long long seg_count(int T, int len) { return 2LL * T / len + 1; }
+DL_HD inline int segs_of(int n, int len) { return (int)(((long long)n + len - 1) / len); }
+// Tokens of a segment (a multiple of `chunk`), or 0 where sequences are not
+// split. `units` blocks (of at most `sms` at a time, one per SM) walk a
+// sequence's chunks in order, so few or uneven sequences leave the GPU idle;
+// split, each segment's end state comes first (about 0.4 of a chunk's time
+// each), then the segments run side by side. One sequence: as many segments as
+// fill the GPU. Several, whose lengths the host does not know: segments of 1.4
+// times an SM's even share, which only a sequence well above it exceeds. Both
+// need at least 4 chunks a segment, and to beat the longest sequence there can
+// be, unsplit, by more than the two launches they cost (about 8 chunks).
+DL_HD inline int seg_len_for(int T, int n_seq, long long units, int chunk, int sms) {
+    const long long chunks = ((long long)T + chunk - 1) / chunk;
+    long long len;
+    if (n_seq == 1) {
+        long long n = sms / units;
+        if (n > chunks / 4) n = chunks / 4;
+        if (n < 2) return 0;
+        len = (chunks + n - 1) / n;
+    } else {
+        len = (7 * chunks * units + 5LL * sms - 1) / (5LL * sms);
+        if (len < 4) len = 4;
+    }
+    if (10 * chunks <= 14 * len + 80) return 0;
+    return (int)(len * chunk);
+}
 
 }  // namespace dl

@@ -225,8 +225,8 @@ cudaError_t launch_ssm_step(const SsmParams &p, const SeqIdx &q, cudaStream_t st
     });
 }
 
-cudaError_t launch_ssm_prompt(const SsmParams &p, const SeqIdx &q, void *, cudaStream_t st) {
-    if (ssm_tc_supported(p)) return launch_ssm_tc(p, q, st);
+cudaError_t launch_ssm_prompt(const SsmParams &p, const SeqIdx &q, void *work, cudaStream_t st) {
+    if (ssm_tc_supported(p)) return launch_ssm_tc(p, q, work, st);
     return dispatch_ssm(p, [&](auto s, auto t, auto dk) -> cudaError_t {
         using ST = decltype(s);
         using IT = decltype(t);
@@ -236,7 +236,5 @@ cudaError_t launch_ssm_prompt(const SsmParams &p, const SeqIdx &q, void *, cudaS
         return cudaGetLastError();
     });
 }
-
-size_t ssm_work_bytes(int, int, int, int, int) { return 0; }
 
 }  // namespace dl

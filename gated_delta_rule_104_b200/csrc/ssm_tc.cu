@@ -14,24 +14,27 @@
 //
 // What is rounded: x, b and c are bfloat16 and enter as they are. P and the
 // state read by C S^T are rounded to bfloat16 once (2^-9 of each term, where y
-// itself is rounded to 2^-9); the addends W go in as a high and a low bfloat16
-// part (2^-18 of each term), so that the state, accumulated and kept in fp32,
-// keeps fp32's accuracy. Every exponent is <= 0: between 32-token blocks the
+// itself is rounded to 2^-9); the addends W go in as three bfloat16 parts, 24
+// bits, so that the state, accumulated and kept in fp32, keeps fp32's accuracy
+// (two parts, 2^-17 of each term, where the state is stored as bfloat16). Every exponent is <= 0: between 32-token blocks the
 // decay is split at the end of the earlier token's block, inside a block it is
 // taken directly. The weights' exponents are sums from the chunk's end
 // backwards, so a token's weight is as accurate as its own exponent is small.
 //
 // One block per (sequence, 128 value rows): one head's, or two heads' of 64
 // that share b and c. It walks the chunks in order with S in tensor memory:
-//   warps 0-3    P from G (thread = token row), then y: read Y, + D x, gate, store
+//   warps 0-3    P from G (thread = token row)
 //   warps 4-7    S: to bfloat16 for C S^T and scaled in place for the next
 //                update (thread = value row); then Y's scaling (thread = token)
-//   warps 8-11   W from X (thread = value row; x is read down a column)
-//   warp 12      TMA: b and x two chunks ahead, c one
-//   warp 13      issues the products: G, C S^T, W^T B, P X
-//   warps 14-15  step sizes and decays of a chunk (one head each), one ahead
-// Each product's time at d_k = 128 is 512 cycles of the tensor pipe, W^T B twice
-// that: 2560 a chunk.
+//   warps 8-15   W from X, 32 tokens at a time, two sets of four warps in turn
+//   warps 16-19  y: read Y, + D x, gate, store (thread = token row)
+//   warp 20      TMA: b and x two chunks ahead, c one
+//   warp 21      issues the products: G, W^T B by 32 tokens, C S^T between them, P X
+//   warps 22-23  step sizes and decays of a chunk (one head each), one ahead
+// Each product's time at d_k = 128 is 512 cycles of the tensor pipe, W^T B three
+// times that: 3072 a chunk. What the other warps issue is as much, so their loops
+// are short (unrolled over a tile they waited for instructions five cycles for
+// each one issued: 320 us where the loops take 234 us, before other changes).
 //
 // What is not a number stays where the recurrence has it: products would
 // spread it, as a weight of zero times NaN is NaN. Rows behind the segment are
@@ -53,18 +56,23 @@ namespace {
 
 using namespace stc;
 
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr int SMS = 148;  // of a B200: the workspace's size must not depend on the device
+
 struct Args {
     SsmParams p;
     SeqIdx q;
     int seg_len;       // tokens of a segment (a multiple of Q)
     int units;         // blocks per segment
-    float *seg_state;  // [segments, H, d_v, d_k]: state in front of each segment (sequences of several)
+    // sequences of several segments, [segments, H, d_v, d_k] and [segments, H]: a
+    // segment's own end state and log decay, then the state in front of it
+    float *seg_state, *seg_decay;
 };
 
 enum Bar {
     C_FULL, C_FREE, B_FULL, B_FREE = B_FULL + 2, X_FULL = B_FREE + 2, X_FREE = X_FULL + 2, SC_FULL = X_FREE + 2,
-    SC_FREE = SC_FULL + 2, S_READY = SC_FREE + 2, W_READY, G_DONE, P_READY, Y2_DONE, YS_READY, Y_DONE, Y_FREE, ST_DONE,
-    ZEROED, DRAIN, BARS
+    SC_FREE = SC_FULL + 2, Z_FULL = SC_FREE + 2, W_FULL = Z_FULL + 12, W_FREE = W_FULL + 2, S_READY = W_FREE + 2, G_DONE, P_READY, Y2_DONE, YS_READY, Y_DONE, Y_FREE, ST_DONE,
+    DRAIN, BARS
 };
 
 __device__ __forceinline__ uint64_t globaltimer() {
@@ -73,21 +81,23 @@ __device__ __forceinline__ uint64_t globaltimer() {
     return t;
 }
 // Wait for the phase of `bar` with parity `par`; gives up after about two
-// seconds, or once another role has (*abort set).
-__device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t par, volatile int *abort) {
-    if (tc::mbar_try_wait(bar, par)) return true;
+// seconds, or once another role has (*abort set). The long wait is a call: the
+// roles' loops have to stay in the instruction caches together.
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t par, volatile int *abort) {
     const uint64_t t0 = globaltimer();
-    for (uint32_t i = 0;; ++i) {
-        if (tc::mbar_try_wait(bar, par)) return true;
-        if ((i & 63u) == 63u) {
-            if (*abort) return false;
-            if (globaltimer() - t0 > 2000000000ull) {
-                *abort = 1;
-                atomicOr(&g_ssm_faults, 1u);
-                return false;
-            }
+    for (;;) {
+        // (suspended for up to 20 us at a time, rather than spinning beside the other roles)
+        if (tc::mbar_try_wait_for(bar, par, 20000u)) return true;
+        if (*abort) return false;
+        if (globaltimer() - t0 > 2000000000ull) {
+            *abort = 1;
+            atomicOr(&g_ssm_faults, 1u);
+            return false;
         }
     }
+}
+__device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t par, volatile int *abort) {
+    return tc::mbar_try_wait(bar, par) || wait_long(bar, par, abort);
 }
 // The same for a whole warp, which leaves together.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t par, volatile int *abort) {
@@ -117,63 +127,143 @@ __device__ __forceinline__ Rows rows_of(const SsmParams &p, int u) {
     }
 }
 
-__device__ __forceinline__ void load_row32(const float *p, float (&v)[32]) { load_vec<32>(p, v); }
-__device__ __forceinline__ void load_row32(const bf16 *p, float (&v)[32]) { load_vec<32>(p, v); }
-__device__ __forceinline__ void store_row32(float *p, const uint32_t (&v)[32]) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) *reinterpret_cast<uint4 *>(p + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+// x where the mask's bits are set, else 0 (a select that the compiler does not turn into branches).
+__device__ __forceinline__ float keep(float x, uint32_t mask) { return __uint_as_float(__float_as_uint(x) & mask); }
+
+// Four 8 x 8 tiles of 16-bit elements from shared memory, transposed.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
-__device__ __forceinline__ void store_row32(bf16 *p, const uint32_t (&v)[32]) {
-    const float *f = reinterpret_cast<const float *>(v);
+// 16 lanes x 16 columns: register 2 n holds lane (thread / 4), column 4 n + thread % 4,
+// register 2 n + 1 the same of lane + 8.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Folds a pair of bfloat16 into `acc`, which turns NaN if one of them is no finite number.
+__device__ __forceinline__ void watch(uint32_t &acc, uint32_t pair) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(pair), "r"(0u));
+}
+__device__ __forceinline__ bool saw_no_number(uint32_t acc) { return (acc & 0x7fff7fffu) != 0; }
+
+// W of a warp's 32 value rows and 32 tokens into a place of tensor memory, 16
+// rows and 16 tokens at a time: x tile xt (from the first of the tokens), their
+// weights w. Each of the TERMS parts holds the leading 8 bits of what the parts
+// before it leave; CLEAN drops parts behind the first that are no finite numbers.
+template <int TERMS, bool CLEAN>
+__device__ __forceinline__ void convert_w(uint32_t trow, uint32_t xt, const float *w, int place, int quad, int lane, uint32_t &acc) {
+    // this lane's row of the transposing loads: token (lane & 7) + 8 (lane >> 4) of
+    // 16, 8 value rows (lane >> 3) & 1 of 16
+    const int mtok = (lane & 7) + ((lane >> 4) << 3), mpiece = 4 * quad + ((lane >> 3) & 1);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {  // 16 value rows
+        uint32_t xr[2][4], part[TERMS][8];
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        *reinterpret_cast<uint4 *>(p + i) = make_uint4(pack_bf2(f[i], f[i + 1]), pack_bf2(f[i + 2], f[i + 3]),
-                                                       pack_bf2(f[i + 4], f[i + 5]), pack_bf2(f[i + 6], f[i + 7]));
+        for (int k = 0; k < 2; ++k) ldmatrix4_trans(xr[k], xt + tile_off(16 * k + mtok, mpiece + 2 * half));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // 8 tokens: this lane's pair of them
+            const float2 ws = *reinterpret_cast<const float2 *>(w + 8 * j + 2 * (lane & 3));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {  // value rows lane / 4 and + 8
+                const uint32_t x = xr[j >> 1][2 * (j & 1) + q];
+                float f0 = bf_lo(x) * ws.x, f1 = bf_hi(x) * ws.y;
+#pragma unroll
+                for (int i = 0; i < TERMS; ++i) {
+                    const uint32_t word = pack_bf2(f0, f1);
+                    part[i][2 * j + q] = word;
+                    if (i == 0) watch(acc, word);
+                    f0 -= bf_lo(word);
+                    f1 -= bf_hi(word);
+                    if constexpr (CLEAN) {
+                        if (!(fabsf(f0) <= 3.4e38f)) f0 = 0.f;
+                        if (!(fabsf(f1) <= 3.4e38f)) f1 = 0.f;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TERMS; ++i) tmem_st_16x16(trow + ((uint32_t)(16 * half) << 16) + w_col(place, i), part[i]);
+    }
 }
 
-// Step sizes and decays of chunk tokens 4 lane .. 4 lane + 3 of one head, by one warp.
+// 16 columns of a state row.
+__device__ __forceinline__ void load_row16(const float *p, float (&v)[16]) { load_vec<16>(p, v); }
+__device__ __forceinline__ void load_row16(const bf16 *p, float (&v)[16]) { load_vec<16>(p, v); }
+__device__ __forceinline__ void store_row16(float *p, const uint32_t (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4 *>(p + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+__device__ __forceinline__ uint4 pack8(const uint32_t *v) {  // floats' bits
+    const float *f = reinterpret_cast<const float *>(v);
+    return make_uint4(pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7]));
+}
+__device__ __forceinline__ void store_row16(bf16 *p, const uint32_t (&v)[16]) {
+    reinterpret_cast<uint4 *>(p)[0] = pack8(v);
+    reinterpret_cast<uint4 *>(p)[1] = pack8(v + 8);
+}
+
+__device__ __noinline__ float softplus_call(float u) { return softplus_f(u); }
+
+// Step sizes and decays of a chunk of one head, by one warp: lane = token of each 32.
 struct Steps {
-    float raw[4];
-    // dt_raw of rows row0 + 4 lane ..; tokens at or behind `m` get no step.
+    float raw[4];  // dt_raw of tokens lane, 32 + lane, ..
+    // Rows row0 + ..; tokens at or behind `m` get no step.
     __device__ __forceinline__ void fetch(const dl_ssm &in, long long row0, int h, int lane, int m) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            raw[j] = 4 * lane + j < m ? to_f(static_cast<const bf16 *>(in.dt)[(row0 + 4 * lane + j) * in.dt_stride + h]) : 0.f;
+            raw[j] = 32 * j + lane < m ? to_f(static_cast<const bf16 *>(in.dt)[(row0 + 32 * j + lane) * in.dt_stride + h]) : 0.f;
     }
-    __device__ __forceinline__ void write(float *sc, float bias, float A, int lane, int m) const {
-        float dt[4], l[4], w[4], sum = 0.f;
+    // Every value of the chunk, before the place for it is free.
+    float dt[4], l[4], u[4], w[4], end;
+    // `behind`: log decay behind the chunk that the weights take in as well.
+    __device__ __forceinline__ void compute(float bias, float A, int lane, int m, float behind) {
+        float before = 0.f;  // log decay in front of the 32 tokens
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            dt[j] = 4 * lane + j < m ? softplus_f(raw[j] + bias) : 0.f;
-            sum += dt[j] * A;
-            l[j] = sum;
+            dt[j] = 32 * j + lane < m ? softplus_call(raw[j] + bias) : 0.f;
+            l[j] = w[j] = dt[j] * A;
         }
-        // sums over the lanes before and behind this one
-        float before = sum, behind = sum;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float a = __shfl_up_sync(0xffffffffu, before, off), b = __shfl_down_sync(0xffffffffu, behind, off);
-            if (lane >= off) before += a;
-            if (lane + off < 32) behind += b;
-        }
-        before = __shfl_up_sync(0xffffffffu, before, 1);
-        behind = __shfl_down_sync(0xffffffffu, behind, 1);
-        if (lane == 0) before = 0.f;
-        if (lane == 31) behind = 0.f;
+        for (int off = 1; off < 32; off <<= 1)
 #pragma unroll
-        for (int j = 3; j >= 0; --j) {
-            w[j] = expf(behind) * dt[j];
-            behind += dt[j] * A;
+            for (int j = 0; j < 4; ++j) {  // sums over the 32 tokens from the front (l) and from behind (w)
+                const float a = __shfl_up_sync(0xffffffffu, l[j], off), b = __shfl_down_sync(0xffffffffu, w[j], off);
+                if (lane >= off) l[j] += a;
+                if (lane + off < 32) w[j] += b;
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
             l[j] += before;
+            before = __shfl_sync(0xffffffffu, l[j], 31);
+            u[j] = expf(before - l[j]) * dt[j];
         }
-        const float end = __shfl_sync(0xffffffffu, l[3], lane | 7);  // l at the end of the lane's 32 tokens
-        *reinterpret_cast<float4 *>(sc + Scal::L + 4 * lane) = make_float4(l[0], l[1], l[2], l[3]);
-        *reinterpret_cast<float4 *>(sc + Scal::U + 4 * lane) =
-            make_float4(expf(end - l[0]) * dt[0], expf(end - l[1]) * dt[1], expf(end - l[2]) * dt[2], expf(end - l[3]) * dt[3]);
-        *reinterpret_cast<float4 *>(sc + Scal::DT + 4 * lane) = make_float4(dt[0], dt[1], dt[2], dt[3]);
-        *reinterpret_cast<float4 *>(sc + Scal::W + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
-        if ((lane & 7) == 7) sc[Scal::RB + (lane >> 3)] = l[3];
-        if (lane == 31) sc[Scal::E] = expf(l[3]);
+        end = before;
+#pragma unroll
+        for (int j = 3; j >= 0; --j) {  // behind: of the 32 tokens
+            const float own = __shfl_down_sync(0xffffffffu, w[j], 1), all = __shfl_sync(0xffffffffu, w[j], 0);
+            w[j] = expf(lane < 31 ? own + behind : behind) * dt[j];
+            behind += all;
+        }
+    }
+    __device__ __forceinline__ void write(float *sc, int lane) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sc[Scal::DT + 32 * j + lane] = dt[j];
+            sc[Scal::L + 32 * j + lane] = l[j] * LOG2E;
+            sc[Scal::U + 32 * j + lane] = u[j];
+            sc[Scal::W + 32 * j + lane] = w[j];
+            if (lane == 31) sc[Scal::RB + j] = l[j] * LOG2E;
+        }
+        if (lane == 31) sc[Scal::E] = expf(end);
     }
 };
 
@@ -192,7 +282,7 @@ __device__ __noinline__ void add_no_numbers(const SsmParams &p, long long row0, 
         const bf16 *b = static_cast<const bf16 *>(in.b) + (row0 + s) * in.b_stride + (long long)g * p.dk;
         float f = 0.f;
         for (int e = 0; e < p.dk; ++e) f = fmaf(to_f(c[e]), to_f(b[e]), f);
-        f *= expf(sc[Scal::L + t] - sc[Scal::L + s]) * sc[Scal::DT + s];
+        f *= exp2f(sc[Scal::L + t] - sc[Scal::L + s]) * sc[Scal::DT + s];
         if (s == t && in.D) f += in.D[h];
         for (int e = 0; e < cols; ++e) {
             const float v = to_f(x[(row0 + s) * in.x_stride + e]);
@@ -204,14 +294,18 @@ __device__ __noinline__ void add_no_numbers(const SsmParams &p, long long row0, 
     }
 }
 
-template <class ST, int DK, int NH>
+template <class ST, int DK, int NH, bool GATE>
 __global__ void __launch_bounds__(THREADS, 1)
 ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_b,
-              const __grid_constant__ CUtensorMap map_c, const __grid_constant__ Args a) {
-    using LY = Layout<DK, NH>;
+              const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_y,
+              const __grid_constant__ CUtensorMap map_z, const __grid_constant__ Args a) {
+    using LY = Layout<DK, NH, GATE>;
     static_assert(LY::N_BAR == BARS, "barriers");
+    // parts of the addends: 24 bits under an fp32 state, 16 under a bfloat16 one
+    constexpr int TERMS = sizeof(ST) == 4 ? 3 : 2;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (aligned by an offset: a pointer made from an integer would be read with generic loads)
+    uint8_t *sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + LY::BAR);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + LY::TSLOT);
     volatile int *abort = reinterpret_cast<volatile int *>(sm + LY::ABORT);
@@ -228,7 +322,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     const int i = seq_of_tile(a.q, tile, a.seg_len, seg);
     if (i < 0 || !seq_range(a.q, i, s0, n)) return;
     const int slot = seq_slot(a.q, i);
-    const int segs = (int)(((long long)n + a.seg_len - 1) / a.seg_len);
+    const int segs = segs_of(n, a.seg_len);
     if (slot < 0 || seg >= segs) return;
     const int len = min(a.seg_len, n - seg * a.seg_len);  // this segment's tokens, from row0
     const int row0 = s0 + seg * a.seg_len, chunks = (len + Q - 1) / Q;
@@ -236,16 +330,16 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     if (tid == 0) {
         auto init = [&](int b, int count) { tc::mbar_init(&bars[b], count); };
         for (int b = 0; b < BARS; ++b) init(b, 1);
-        for (int b : {(int)S_READY, (int)W_READY, (int)P_READY, (int)YS_READY, (int)Y_FREE, (int)ZEROED}) init(b, 4);
+        for (int b : {(int)S_READY, (int)W_FULL, (int)W_FULL + 1, (int)P_READY, (int)YS_READY, (int)Y_FREE}) init(b, 4);
         for (int k = 0; k < 2; ++k) {
             init(X_FREE + k, 4);
             init(SC_FULL + k, NH);
-            init(SC_FREE + k, 12);
+            init(SC_FREE + k, 20);
         }
         *abort = 0;
         tc::mbar_init_fence();
     }
-    if (warp == 13) {
+    if (warp == 21) {
         tc::tmem_alloc(tslot, T_COLS);
         tc::tmem_relinquish();
     }
@@ -259,7 +353,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     };
 
     if (warp < 4) {
-        // ------------------------------------------------ P from G, and y (thread = token row t)
+        // ------------------------------------------------ P from G (thread = token row t)
         const int quad = warp, t = 32 * quad + lane;
         const uint32_t trow = tb + ((uint32_t)(32 * quad) << 16);
         for (int c = 0; c < chunks; ++c) {
@@ -267,102 +361,59 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             if (!wait_warp(&bars[SC_FULL + par], par2, abort)) break;
             if (!wait_warp(&bars[G_DONE], par, abort)) break;
             tc::tc_fence_after();
-#pragma unroll 1
-            for (int kb = 0; kb < 4; ++kb) {
-                uint32_t pw[NH][16];
-                if (kb <= quad) {
-                    uint32_t gr[32];
-                    tc::tmem_ld32(trow + T_G + 32 * kb, gr);
-                    tc::tmem_wait_ld();
+            uint32_t r0[16], r1[16];  // 16 columns each, one being loaded
+            tc::tmem_ld16(trow + T_G, r0);
+            // P of tokens 16 k .. 16 k + 15 from their scores
+            auto decayed = [&](int k, const uint32_t (&g)[16], bool diagonal) {
+                uint32_t pw[8];
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        const float *sc = scal(c, h);
-                        const float lt = sc[Scal::L + t];
-                        if (kb < quad) {
-                            const float v = __expf(lt - sc[Scal::RB + kb]);
+                for (int h = 0; h < NH; ++h) {
+                    const float *sc = scal(c, h);
+                    const float lt = sc[Scal::L + t];
+                    if (!diagonal) {
+                        const float v = exp2_fast(lt - sc[Scal::RB + (k >> 1)]);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 u = *reinterpret_cast<const float4 *>(sc + Scal::U + 32 * kb + e);
-                                pw[h][e / 2] = pack_bf2(__uint_as_float(gr[e]) * (u.x * v), __uint_as_float(gr[e + 1]) * (u.y * v));
-                                pw[h][e / 2 + 1] =
-                                    pack_bf2(__uint_as_float(gr[e + 2]) * (u.z * v), __uint_as_float(gr[e + 3]) * (u.w * v));
-                            }
-                        } else {  // the block on the diagonal: tokens up to t
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 u = *reinterpret_cast<const float4 *>(sc + Scal::U + 16 * k + e);
+                            pw[e / 2] = pack_bf2(__uint_as_float(g[e]) * (u.x * v), __uint_as_float(g[e + 1]) * (u.y * v));
+                            pw[e / 2 + 1] = pack_bf2(__uint_as_float(g[e + 2]) * (u.z * v), __uint_as_float(g[e + 3]) * (u.w * v));
+                        }
+                    } else {  // tokens up to t
+                        const int ahead = 16 * k - t - 1;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 l = *reinterpret_cast<const float4 *>(sc + Scal::L + 32 * kb + e);
-                                const float4 d = *reinterpret_cast<const float4 *>(sc + Scal::DT + 32 * kb + e);
-                                const float f0 = e <= lane ? __uint_as_float(gr[e]) * (__expf(lt - l.x) * d.x) : 0.f;
-                                const float f1 = e + 1 <= lane ? __uint_as_float(gr[e + 1]) * (__expf(lt - l.y) * d.y) : 0.f;
-                                const float f2 = e + 2 <= lane ? __uint_as_float(gr[e + 2]) * (__expf(lt - l.z) * d.z) : 0.f;
-                                const float f3 = e + 3 <= lane ? __uint_as_float(gr[e + 3]) * (__expf(lt - l.w) * d.w) : 0.f;
-                                pw[h][e / 2] = pack_bf2(f0, f1);
-                                pw[h][e / 2 + 1] = pack_bf2(f2, f3);
-                            }
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 l = *reinterpret_cast<const float4 *>(sc + Scal::L + 16 * k + e);
+                            const float4 d = *reinterpret_cast<const float4 *>(sc + Scal::DT + 16 * k + e);
+                            const float lv[4] = {l.x, l.y, l.z, l.w}, dv[4] = {d.x, d.y, d.z, d.w};
+                            float o[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                o[i] = keep(__uint_as_float(g[e + i]) * (exp2_fast(lt - lv[i]) * dv[i]), (uint32_t)((ahead + e + i) >> 31));
+                            pw[e / 2] = pack_bf2(o[0], o[1]);
+                            pw[e / 2 + 1] = pack_bf2(o[2], o[3]);
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < NH; ++h)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pw[h][e] = 0u;
+                    tc::tmem_st8(trow + p_col(k, h), pw);
                 }
+            };
+#pragma unroll 1
+            for (int kb = 0; kb <= quad; ++kb) {  // 32 tokens s
+                tc::tmem_wait_ld();
+                tc::tmem_ld16(trow + T_G + 32 * kb + 16, r1);
+                decayed(2 * kb, r0, kb == quad);
+                tc::tmem_wait_ld();
+                if (kb < quad) tc::tmem_ld16(trow + T_G + 32 * kb + 32, r0);
+                decayed(2 * kb + 1, r1, kb == quad);
+            }
+#pragma unroll 1
+            for (int k = 2 * quad + 2; k < 8; ++k) {  // tokens behind every t of the warp
+                uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int h = 0; h < NH; ++h) tc::tmem_st16(trow + p_col(2 * kb, h), pw[h]);
+                for (int h = 0; h < NH; ++h) tc::tmem_st8(trow + p_col(k, h), zero);
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
             arrive(P_READY);
-
-            // y of row t: Y + D x, gated
-            const int m = min(Q, len - c * Q);
-            const long long row = (long long)row0 + c * Q + t;
-            if (!wait_warp(&bars[Y_DONE], par, abort)) break;
-            tc::tc_fence_after();
-            const uint8_t *xt = sm + LY::x(par);
-#pragma unroll 1
-            for (int cb = 0; cb < 4; ++cb) {
-                const int h = NH == 2 ? cb >> 1 : 0, col = rw.r0 + (NH == 2 ? (cb & 1) * 32 : cb * 32);
-                const bool live = t < m && (h == 0 || rw.two);
-                uint4 zr[4];
-                if (in.z && live) {
-                    const uint4 *z = reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(in.z) + row * in.z_stride +
-                                                                     (long long)(rw.h0 + h) * p.dv + col);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) zr[j] = z[j];
-                }
-                uint32_t yr[32];
-                tc::tmem_ld32(trow + T_Y + 32 * cb, yr);
-                tc::tmem_wait_ld();
-                if (!live) continue;
-                const float D = in.D ? in.D[rw.h0 + h] : 0.f;
-                uint4 *y = reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.y) + (row * p.H + rw.h0 + h) * p.dv + col);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float x[8], o[8];
-                    StateVec<bf16>::unpack(*reinterpret_cast<const uint4 *>(xt + tile_off(t, 4 * cb + j)), x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = fmaf(D, x[e], __uint_as_float(yr[8 * j + e]));
-                    if (in.z) {
-                        float z[8];
-                        StateVec<bf16>::unpack(zr[j], z);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] *= silu_f<bf16>(z[e]);
-                    }
-                    y[j] = StateVec<bf16>::pack(o);
-                }
-            }
-            tc::tc_fence_before();
-            arrive(Y_FREE);
-            const uint32_t *nf = reinterpret_cast<const uint32_t *>(sm + LY::NF) + 16 * par;
-            uint32_t any = 0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) any |= nf[j];
-            if (any && t < m)
-                for (int h = 0; h < NH; ++h)
-                    if (h == 0 || rw.two)
-                        add_no_numbers(p, (long long)row0 + c * Q, t, nf, scal(c, h), rw.h0 + h, rw.g, rw.r0, R / NH);
-            arrive(X_FREE + par);
             arrive(SC_FREE + par);
         }
     } else if (warp < 8) {
@@ -381,34 +432,43 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 if (!(ok = wait_warp(&bars[ST_DONE], (c - 1) & 1, abort))) break;
                 tc::tc_fence_after();
             }
+            uint32_t r0[16], r1[16];  // 16 columns each, one being loaded
+            // 16 key columns: rounded for C S^T, and decayed by this chunk
+            auto advance = [&](int k, uint32_t (&v)[16]) {
+                uint8_t *dst = sm + LY::S + (k >> 2) * PANEL + r * 128;
+                *reinterpret_cast<uint4 *>(dst + (((32 * k) & 127) ^ ((r & 7) << 4))) = pack8(v);
+                *reinterpret_cast<uint4 *>(dst + (((32 * k + 16) & 127) ^ ((r & 7) << 4))) = pack8(v + 8);
 #pragma unroll
-            for (int cb = 0; cb < DK / 32; ++cb) {
-                uint32_t v[32];
-                if (c > 0) {
-                    tc::tmem_ld32(trow + T_S + 32 * cb, v);
-                    tc::tmem_wait_ld();
-                } else {
-                    float f[32];
+                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * e);
+                tc::tmem_st16(trow + T_S + 16 * k, v);
+            };
+            if (c == 0) {  // the state in front of the segment
+#pragma unroll 1
+                for (int k = 0; k < DK / 16; ++k) {
+                    float f[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) f[j] = 0.f;
+                    for (int j = 0; j < 16; ++j) f[j] = 0.f;
                     if (live) {
                         if (segs > 1)
-                            load_row32(a.seg_state + ((long long)(seg_base(s0, a.seg_len) + seg) * p.H * p.dv + srow) * DK + 32 * cb, f);
+                            load_row16(a.seg_state + ((long long)(seg_base(s0, a.seg_len) + seg) * p.H * p.dv + srow) * DK + 16 * k, f);
                         else
-                            load_row32(S + 32 * cb, f);
+                            load_row16(S + 16 * k, f);
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(f[j]);
+                    for (int j = 0; j < 16; ++j) r0[j] = __float_as_uint(f[j]);
+                    advance(k, r0);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float *f = reinterpret_cast<const float *>(v) + 8 * j;
-                    *reinterpret_cast<uint4 *>(sm + LY::S + tile_off(r, 4 * cb + j)) = make_uint4(
-                        pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7]));
+            } else {
+                tc::tmem_ld16(trow + T_S, r0);
+#pragma unroll 1
+                for (int k = 0; k < DK / 16; k += 2) {
+                    tc::tmem_wait_ld();
+                    tc::tmem_ld16(trow + T_S + 16 * k + 16, r1);
+                    advance(k, r0);
+                    tc::tmem_wait_ld();
+                    if (k + 2 < DK / 16) tc::tmem_ld16(trow + T_S + 16 * k + 32, r0);
+                    advance(k + 1, r1);
                 }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * e);
-                tc::tmem_st32(trow + T_S + 32 * cb, v);
             }
             tc::fence_async_smem();
             tc::tmem_wait_st();
@@ -417,18 +477,25 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 
             float ex[NH];
 #pragma unroll
-            for (int k = 0; k < NH; ++k) ex[k] = __expf(scal(c, k)[Scal::L + r]);
+            for (int k = 0; k < NH; ++k) ex[k] = exp2_fast(scal(c, k)[Scal::L + r]);
             arrive(SC_FREE + par);
             if (!(ok = wait_warp(&bars[Y2_DONE], par, abort))) break;
             tc::tc_fence_after();
+            tc::tmem_ld16(trow + T_Y, r0);
+            auto scale = [&](int k, uint32_t (&v)[16]) {
+                const float f = NH == 2 && k >= 4 ? ex[NH - 1] : ex[0];
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb) {
-                uint32_t v[32];
-                tc::tmem_ld32(trow + T_Y + 32 * cb, v);
+                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                tc::tmem_st16(trow + T_Y + 16 * k, v);
+            };
+#pragma unroll 1
+            for (int k = 0; k < 8; k += 2) {
                 tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * ex[NH == 2 ? cb >> 1 : 0]);
-                tc::tmem_st32(trow + T_Y + 32 * cb, v);
+                tc::tmem_ld16(trow + T_Y + 16 * k + 16, r1);
+                scale(k, r0);
+                tc::tmem_wait_ld();
+                if (k + 2 < 8) tc::tmem_ld16(trow + T_Y + 16 * k + 32, r0);
+                scale(k + 1, r1);
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -436,20 +503,19 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         }
         if (ok && wait_warp(&bars[ST_DONE], (chunks - 1) & 1, abort) && seg == segs - 1) {
             tc::tc_fence_after();
-#pragma unroll
-            for (int cb = 0; cb < DK / 32; ++cb) {
-                uint32_t v[32];
-                tc::tmem_ld32(trow + T_S + 32 * cb, v);
+#pragma unroll 1
+            for (int k = 0; k < DK / 16; ++k) {
+                uint32_t v[16];
+                tc::tmem_ld16(trow + T_S + 16 * k, v);
                 tc::tmem_wait_ld();
-                if (live) store_row32(S + 32 * cb, v);
+                if (live) store_row16(S + 16 * k, v);
             }
             tc::tc_fence_before();
         }
-    } else if (warp < 12) {
-        // ------------------------------------------------ W from X (thread = value row r)
-        const int quad = warp & 3, r = 32 * quad + lane, h = NH == 2 ? r >> 6 : 0;
+    } else if (warp < 16) {
+        // ------------------------------------------------ W from X (a warp's 32 value rows), every other 32 tokens
+        const int quad = warp & 3, place = (warp - 8) >> 2, r = 32 * quad + lane, h = NH == 2 ? r >> 6 : 0;
         const uint32_t trow = tb + ((uint32_t)(32 * quad) << 16);
-        const int piece = r >> 3, in_piece = (r & 7) * 2;
         uint32_t *nf = reinterpret_cast<uint32_t *>(sm + LY::NF) + 4 * quad;
         for (int c = 0; c < chunks; ++c) {
             const uint32_t par = c & 1, par2 = (c >> 1) & 1;
@@ -457,81 +523,165 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             uint8_t *xt = sm + LY::x(par);
             if (!wait_warp(&bars[X_FULL + par], par2, abort)) break;
             if (!wait_warp(&bars[SC_FULL + par], par2, abort)) break;
-            if (m < Q) {  // (the last chunk) zeros behind the segment, in X and B
-                if (!wait_warp(&bars[B_FULL + par], par2, abort)) break;
-                constexpr int XP = R / 8, BP = DK / 8;
-                for (int k = tid - 256; k < (Q - m) * (XP + BP); k += 128) {
-                    const int row = m + k / (XP + BP), pc = k % (XP + BP);
-                    uint8_t *dst = pc < XP ? xt + tile_off(row, pc) : sm + LY::b(par) + tile_off(row, pc - XP);
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                tc::fence_async_smem();
-                arrive(ZEROED);
-                if (!wait_warp(&bars[ZEROED], 0, abort)) break;
-            }
+            if (m < Q && !wait_warp(&bars[B_FULL + par], par2, abort)) break;
             const float *w = scal(c, h) + Scal::W;
-            float no_number = 0.f;  // NaN once an x is no finite number
             bool ok = true;
 #pragma unroll 1
-            for (int kb = 0; kb < 4; ++kb) {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 w4 = *reinterpret_cast<const float4 *>(w + 32 * kb + e);
-                    const float ws[4] = {w4.x, w4.y, w4.z, w4.w};
-                    float f[4], rest[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int s = e + k;  // (row 32 kb + s: the same position in its 8 rows)
-                        const float x = to_f(*reinterpret_cast<const bf16 *>(
-                            xt + (piece >> 3) * PANEL + (32 * kb + s) * 128 + (((piece & 7) ^ (s & 7)) << 4) + in_piece));
-                        no_number = fmaf(x, 0.f, no_number);
-                        f[k] = x * ws[k];
+            for (int q = place; q < 4; q += 2) {  // 32 tokens
+                const int nq = 4 * c + q;
+                if (32 * q + 32 > m) {  // (the last chunk) zeros behind the segment, in X and B
+                    constexpr int BP = DK / 32;  // pieces of a row of b for each warp
+                    for (int k = lane; k < 32 * (4 + BP); k += 32) {
+                        const int row = 32 * q + k / (4 + BP), pc = k % (4 + BP);
+                        uint8_t *dst = pc < 4 ? xt + tile_off(row, 4 * quad + pc) : sm + LY::b(par) + tile_off(row, BP * quad + pc - 4);
+                        if (row >= m) *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
                     }
-#pragma unroll
-                    for (int k = 0; k < 4; k += 2) {
-                        const uint32_t hw = pack_bf2(f[k], f[k + 1]);
-                        rest[k] = f[k] - bf_lo(hw);
-                        rest[k + 1] = f[k + 1] - bf_hi(hw);
-                        if (!(fabsf(rest[k]) <= 3.4e38f)) rest[k] = 0.f;
-                        if (!(fabsf(rest[k + 1]) <= 3.4e38f)) rest[k + 1] = 0.f;
-                        hi[(e + k) / 2] = hw;
-                        lo[(e + k) / 2] = pack_bf2(rest[k], rest[k + 1]);
-                    }
+                    tc::fence_async_smem();
+                    __syncwarp();
                 }
-                if (kb == 0 && c > 0) {  // the previous update has read W
-                    if (!(ok = wait_warp(&bars[ST_DONE], (c - 1) & 1, abort))) break;
+                if (nq >= 2) {  // the update that used this place has read it
+                    if (!(ok = wait_warp(&bars[W_FREE + place], (uint32_t)((nq >> 1) - 1) & 1, abort))) break;
                     tc::tc_fence_after();
                 }
-                tc::tmem_st16(trow + T_W + 16 * kb, hi);
-                tc::tmem_st16(trow + T_WLO + 16 * kb, lo);
-            }
-            if (!ok) break;
-            arrive(SC_FREE + par);
-            uint32_t mask[4] = {0u, 0u, 0u, 0u};
-            if (__any_sync(0xffffffffu, !(no_number == 0.f))) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                uint32_t acc = 0u, mask = 0u;
+                const uint32_t xq = tc::smem_u32(xt) + 32 * 128 * q;
+                convert_w<TERMS, false>(trow, xq, w + 32 * q, place, quad, lane, acc);
+                if (__any_sync(0xffffffffu, saw_no_number(acc))) {
+                    // again, without later parts that are no numbers; then x's own zeroed
+                    convert_w<TERMS, true>(trow, xq, w + 32 * q, place, quad, lane, acc);
                     for (int s = 0; s < 32; ++s) {
-                        bf16 *xp = reinterpret_cast<bf16 *>(xt + tile_off(32 * j + s, piece) + in_piece);
+                        bf16 *xp = reinterpret_cast<bf16 *>(xt + tile_off(32 * q + s, r >> 3) + (r & 7) * 2);
                         if (!(fabsf(to_f(*xp)) <= 3.4e38f)) {
                             *xp = __float2bfloat16_rn(0.f);
-                            mask[j] |= 1u << s;
+                            mask |= 1u << s;
                         }
                     }
-                    mask[j] = __reduce_or_sync(0xffffffffu, mask[j]);
+                    mask = __reduce_or_sync(0xffffffffu, mask);
+                    tc::fence_async_smem();
                 }
-                tc::fence_async_smem();
+                if (lane == 0) nf[16 * par + q] = mask;
+                if (q >= 2) arrive(SC_FREE + par);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                arrive(W_FULL + place);
             }
-            if (lane == 0) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) nf[16 * par + j] = mask[j];
-            }
-            tc::tmem_wait_st();
-            tc::tc_fence_before();
-            arrive(W_READY);
+            if (!ok) break;
         }
-    } else if (warp == 12) {
+    } else if (warp >= 16 && warp < 20) {
+        // ------------------------------------------------ y (thread = token row t)
+        const int quad = warp & 3, t = 32 * quad + lane;
+        const uint32_t trow = tb + ((uint32_t)(32 * quad) << 16);
+        float D[NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) D[h] = in.D && (h == 0 || rw.two) ? in.D[rw.h0 + h] : 0.f;
+        // the gate of the warp's rows: blocks of 32 columns, four a chunk, three in flight
+        int nz = 0;
+        auto load_z = [&]() {
+            if (GATE && lane == 0 && nz < 4 * chunks) {
+                uint64_t *full = &bars[Z_FULL + 3 * quad + nz % 3];
+                tc::mbar_arrive_expect_tx(full, LY::ZBLOCK);
+                tc::tma_load_2d(sm + LY::z(quad, nz % 3), &map_z, rw.col0 + 32 * (nz & 3), row0 + (nz >> 2) * Q + 32 * quad, full);
+                ++nz;
+            }
+        };
+        if constexpr (GATE)
+            for (int k = 0; k < 3; ++k) load_z();
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t par = c & 1;
+            if (c > 0) {  // the previous chunk's stores have read x's place: it may be loaded again
+                if (lane == 0) tc::bulk_wait_read<0>();
+                arrive(X_FREE + (par ^ 1));
+            }
+
+            // y of row t: Y + D x, gated; through x's place in shared memory to
+            // HBM by TMA, or straight from registers where the warp's 32 rows
+            // reach behind the segment (or x holds what is no number)
+            const int m = min(Q, len - c * Q);
+            const long long row = (long long)row0 + c * Q + t;
+            if (!wait_warp(&bars[Y_DONE], par, abort)) break;
+            tc::tc_fence_after();
+            const uint4 *nf = reinterpret_cast<const uint4 *>(sm + LY::NF) + 4 * par;
+            uint32_t any = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) any |= nf[j].x | nf[j].y | nf[j].z | nf[j].w;
+            const bool direct = any || 32 * quad + 32 > m;
+            uint8_t *xt = sm + LY::x(par);
+            uint32_t r0[16], r1[16];  // 16 columns each, one being loaded
+            tc::tmem_ld16(trow + T_Y, r0);
+            uint8_t *xrow = xt + t * 128;
+            const uint32_t swz = (t & 7) << 4;
+            auto x_at = [&](int k, int j) {  // 8 of 16 value columns
+                return reinterpret_cast<uint4 *>(xrow + (k >> 2) * PANEL + (((32 * k + 16 * j) & 127) ^ swz));
+            };
+            auto columns = [&](auto direct_c) {
+                auto finish = [&](int k, const uint32_t (&y)[16], uint4 x0, uint4 x1, const uint8_t *zrow) {
+                    const int h = NH == 2 ? k >> 2 : 0;
+                    const float d = h ? D[NH - 1] : D[0];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float x[8], o[8];
+                        StateVec<bf16>::unpack(j ? x1 : x0, x);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = fmaf(d, x[e], __uint_as_float(y[8 * j + e]));
+                        if constexpr (GATE) {
+                            float z[8];
+                            StateVec<bf16>::unpack(*reinterpret_cast<const uint4 *>(zrow + gate_off(lane, 2 * (k & 1) + j)), z);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] *= silu_f<bf16>(z[e]);
+                        }
+                        const uint4 out = StateVec<bf16>::pack(o);
+                        if constexpr (!decltype(direct_c)::value)
+                            *x_at(k, j) = out;
+                        else if (t < m && (h == 0 || rw.two))
+                            reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.y) + row * p.H * p.dv + rw.col0)[2 * k + j] = out;
+                    }
+                };
+#pragma unroll 1
+                for (int cb = 0; cb < 4; ++cb) {  // 32 value columns
+                    const int zi = 4 * c + cb;
+                    const uint4 xa = *x_at(2 * cb, 0), xb = *x_at(2 * cb, 1), xc = *x_at(2 * cb + 1, 0), xd = *x_at(2 * cb + 1, 1);
+                    if (GATE && !wait_warp(&bars[Z_FULL + 3 * quad + zi % 3], (zi / 3) & 1, abort)) return false;
+                    const uint8_t *zrow = sm + LY::z(quad, GATE ? zi % 3 : 0);
+                    tc::tmem_wait_ld();
+                    tc::tmem_ld16(trow + T_Y + 32 * cb + 16, r1);
+                    finish(2 * cb, r0, xa, xb, zrow);
+                    tc::tmem_wait_ld();
+                    if (cb < 3) tc::tmem_ld16(trow + T_Y + 32 * cb + 32, r0);
+                    finish(2 * cb + 1, r1, xc, xd, zrow);
+                    if constexpr (GATE) {
+                        __syncwarp();
+                        load_z();
+                    }
+                }
+                return true;
+            };
+            if (!(direct ? columns(std::true_type{}) : columns(std::false_type{}))) break;
+            tc::tc_fence_before();
+            arrive(Y_FREE);
+            if (!direct) {
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    for (int k = 0; k < (NH == 2 && !rw.two ? 1 : R / 64); ++k)
+                        tc::tma_store_2d(&map_y, rw.col0 + 64 * k, row0 + c * Q + 32 * quad, xt + k * PANEL + quad * 4096);
+                    tc::bulk_commit();
+                }
+            } else if (any && t < m) {
+                for (int h = 0; h < NH; ++h)
+                    if (h == 0 || rw.two)
+                        add_no_numbers(p, (long long)row0 + c * Q, t, reinterpret_cast<const uint32_t *>(nf), scal(c, h), rw.h0 + h,
+                                       rw.g, rw.r0, R / NH);
+            }
+            arrive(SC_FREE + par);
+        }
+        if (lane == 0) {  // the warp's last copies have landed
+            tc::bulk_wait_all();
+            for (int k = 0; GATE && k < 3; ++k) {
+                const int n = (nz + 2 - k) / 3;
+                if (n) drain(&bars[Z_FULL + 3 * quad + k], (n - 1) & 1);
+            }
+        }
+    } else if (warp == 20) {
         // ------------------------------------------------ loads
         if (lane == 0) {
             tc::tma_prefetch_desc(&map_x);
@@ -570,50 +720,71 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             if (nc) drain(&bars[C_FULL], (nc - 1) & 1);
         }
         __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == 21) {
         // ------------------------------------------------ products
         if (lane == 0) {
             constexpr uint32_t ID_G = tc::instr_desc(tc::FMT_BF16, false, false, Q, Q);
             constexpr uint32_t ID_Y2 = tc::instr_desc(tc::FMT_BF16, false, false, Q, R);
             constexpr uint32_t ID_Y1 = tc::instr_desc(tc::FMT_BF16, false, true, Q, R / NH);
             constexpr uint32_t ID_S = tc::instr_desc(tc::FMT_BF16, false, true, R, DK);
-            const uint32_t ct = tc::smem_u32(sm + LY::C), st = tc::smem_u32(sm + LY::S);
-            // 16 columns of K of a tile whose rows are the product's rows or columns
-            auto kmajor = [](uint32_t tile, int k) {
-                return tc::smem_desc(tile + (k >> 2) * PANEL + (k & 3) * 32, 16, 1024, tc::SWZ_128);
-            };
-            // 16 rows of K of a tile whose columns are the product's columns
-            auto nmajor = [](uint32_t tile, int k) { return tc::smem_desc(tile + k * 2048, PANEL, 1024, tc::SWZ_128); };
+            // descriptors of the tiles' first 16 columns (K along the columns: the
+            // tile's rows are the product's rows or columns), and of the first 16
+            // rows (K along the rows: its columns are the product's columns); those
+            // of the others differ by a constant (in 16-byte units)
+            auto kmajor = [&](int off) { return tc::smem_desc(tc::smem_u32(sm + off), 16, 1024, tc::SWZ_128); };
+            auto nmajor = [&](int off) { return tc::smem_desc(tc::smem_u32(sm + off), PANEL, 1024, tc::SWZ_128); };
+            constexpr uint64_t COLS = 32 / 16, PANELS = PANEL / 16, ROWS = 16 * 128 / 16;
+            const uint64_t ck = kmajor(LY::C), sk = kmajor(LY::S);
+            const uint64_t bk[2] = {kmajor(LY::b(0)), kmajor(LY::b(1))}, bn[2] = {nmajor(LY::b(0)), nmajor(LY::b(1))},
+                           xn[2] = {nmajor(LY::x(0)), nmajor(LY::x(1))};
             bool ok = true;
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t par = c & 1, par2 = (c >> 1) & 1;
-                const uint32_t bt = tc::smem_u32(sm + LY::b(par)), xt = tc::smem_u32(sm + LY::x(par));
+                // A B^T over DK columns of two tiles
+                auto over_columns = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t id) {
+#pragma unroll
+                    for (int pn = 0; pn < LY::KP; ++pn)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_ss_f16(d, ad + pn * PANELS + k * COLS, bd + pn * PANELS + k * COLS, id, pn + k > 0);
+                };
+                // S' of 64 tokens
+                auto update = [&](int half) {
+                    const uint64_t bd = (par ? bn[1] : bn[0]) + half * 4 * ROWS;
+#pragma unroll
+                    for (int place = 0; place < 2; ++place) {
+                        if (!wait1(&bars[W_FULL + place], (uint32_t)half, abort)) return false;  // (two uses a chunk)
+                        tc::tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < TERMS; ++i)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                tc::mma_ts_f16(tb + T_S, tb + w_col(place, i) + 8 * k, bd + (2 * place + k) * ROWS, ID_S, true);
+                        tc::mma_commit(&bars[W_FREE + place]);
+                    }
+                    return true;
+                };
                 if (!(ok = wait1(&bars[C_FULL], par, abort) && wait1(&bars[B_FULL + par], par2, abort))) break;
                 tc::tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k) tc::mma_ss_f16(tb + T_G, kmajor(ct, k), kmajor(bt, k), ID_G, k > 0);
+                over_columns(tb + T_G, ck, par ? bk[1] : bk[0], ID_G);
                 tc::mma_commit(&bars[G_DONE]);
-                if (!(ok = wait1(&bars[S_READY], par, abort) && (c == 0 || wait1(&bars[Y_FREE], (c - 1) & 1, abort)))) break;
+                if (!(ok = wait1(&bars[S_READY], par, abort) && update(0))) break;
+                if (!(ok = c == 0 || wait1(&bars[Y_FREE], (c - 1) & 1, abort))) break;
                 tc::tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k) tc::mma_ss_f16(tb + T_Y, kmajor(ct, k), kmajor(st, k), ID_Y2, k > 0);
+                over_columns(tb + T_Y, ck, sk, ID_Y2);
                 tc::mma_commit(&bars[Y2_DONE]);
                 tc::mma_commit(&bars[C_FREE]);
-                if (!(ok = wait1(&bars[W_READY], par, abort))) break;
-                tc::tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < Q / 16; ++k) tc::mma_ts_f16(tb + T_S, tb + T_W + 8 * k, nmajor(bt, k), ID_S, true);
-#pragma unroll
-                for (int k = 0; k < Q / 16; ++k) tc::mma_ts_f16(tb + T_S, tb + T_WLO + 8 * k, nmajor(bt, k), ID_S, true);
+                if (!(ok = update(1))) break;
                 tc::mma_commit(&bars[ST_DONE]);
                 tc::mma_commit(&bars[B_FREE + par]);
                 if (!(ok = wait1(&bars[P_READY], par, abort) && wait1(&bars[YS_READY], par, abort))) break;
                 tc::tc_fence_after();
+                const uint64_t xd = par ? xn[1] : xn[0];
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
                     for (int k = 0; k < Q / 16; ++k)
-                        tc::mma_ts_f16(tb + T_Y + (R / NH) * h, tb + p_col(k, h), nmajor(xt + h * PANEL, k), ID_Y1, true);
+                        tc::mma_ts_f16(tb + T_Y + (R / NH) * h, tb + p_col(k, h), xd + h * PANELS + k * ROWS, ID_Y1, true);
                 tc::mma_commit(&bars[Y_DONE]);
             }
             if (!ok) {  // products in flight have completed before tensor memory is freed
@@ -622,70 +793,315 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             }
         }
         __syncwarp();
-    } else if (warp - 14 < NH) {
+    } else if (warp - 22 < NH) {
         // ------------------------------------------------ step sizes and decays of head h
-        const int h = warp - 14;
+        const int h = warp - 22;
         const bool live = h == 0 || rw.two;
         const float A = live ? in.A[rw.h0 + h] : 0.f, bias = live && in.dt_bias ? in.dt_bias[rw.h0 + h] : 0.f;
-        Steps next;
-        next.fetch(in, row0, rw.h0 + h, lane, live ? len : 0);
+        Steps st;
+        st.fetch(in, row0, rw.h0 + h, lane, live ? len : 0);
         for (int c = 0; c < chunks; ++c) {
-            const Steps now = next;
             const int m = live ? len - c * Q : 0;
-            next.fetch(in, (long long)row0 + (c + 1) * Q, rw.h0 + h, lane, m - Q);
+            st.compute(bias, A, lane, m, 0.f);
+            st.fetch(in, (long long)row0 + (c + 1) * Q, rw.h0 + h, lane, m - Q);
             if (c >= 2 && !wait_warp(&bars[SC_FREE + (c & 1)], (uint32_t)((c >> 1) - 1) & 1, abort)) break;
-            now.write(scal(c, h), bias, A, lane, m);
+            st.write(scal(c, h), lane);
             arrive(SC_FULL + (c & 1));
         }
     }
     __syncthreads();
-    if (warp == 13) {
+    if (warp == 21) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tb, T_COLS);
     }
 }
 
-// A [rows, cols] bfloat16 matrix with a row stride, in boxes of Q rows of 64 columns.
-cudaError_t row_map(CUtensorMap *m, const void *base, long long cols, long long rows, long long stride) {
+// The end state of every segment but a sequence's last, from a state of zero,
+// and its log decay: the scan's state products alone, over the chunks from the
+// last to the first, so that each token's weight takes in the decay behind its
+// chunk and the state needs no scaling. Three parts always: what is summed here
+// reaches the last state.
+constexpr int END_THREADS = 384;
+
+template <int DK, int NH>
+__global__ void __launch_bounds__(END_THREADS, 1)
+ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ Args a) {
+    using LY = EndLayout<DK, NH>;
+    constexpr int TERMS = 3;
+    enum { B_FULL, FREE = B_FULL + 2, X_FULL = FREE + 2, SC_FULL = X_FULL + 2, SC_FREE = SC_FULL + 2, W_FULL = SC_FREE + 2,
+           W_FREE = W_FULL + 2, DONE = W_FREE + 2, BARS };
+    static_assert(LY::N_BAR == BARS, "barriers");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + LY::BAR);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + LY::TSLOT);
+    volatile int *abort = reinterpret_cast<volatile int *>(sm + LY::ABORT);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const SsmParams &p = a.p;
+    const dl_ssm &in = p.in;
+
+    const int tile = (int)(blockIdx.x / (unsigned)a.units);
+    const Rows rw = rows_of<NH>(p, (int)(blockIdx.x - (unsigned)tile * a.units));
+    int seg = 0, s0, n;
+    const int i = seq_of_tile(a.q, tile, a.seg_len, seg, 0);
+    if (i < 0 || !seq_range(a.q, i, s0, n)) return;
+    if (seq_slot(a.q, i) < 0 || seg >= segs_of(n, a.seg_len) - 1) return;
+    const int row0 = s0 + seg * a.seg_len, chunks = a.seg_len / Q;
+    const long long out = (long long)seg_base(s0, a.seg_len) + seg;
+
+    if (tid == 0) {
+        for (int b = 0; b < BARS; ++b) {
+            const bool sc_full = b >= SC_FULL && b < SC_FREE, sc_free = b >= SC_FREE && b < W_FULL, w_full = b >= W_FULL && b < W_FREE;
+            tc::mbar_init(&bars[b], sc_full ? NH : sc_free ? 8 : w_full ? 4 : 1);
+        }
+        *abort = 0;
+        tc::mbar_init_fence();
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(tslot, T_COLS);
+        tc::tmem_relinquish();
+    }
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tb = *tslot;
+    auto weights = [&](int c, int h) { return reinterpret_cast<float *>(sm + LY::scal(c & 1, h)); };
+    auto arrive = [&](int b) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars[b]);
+    };
+
+    if (warp < 8) {
+        // ------------------------------------------------ W, every other 32 tokens; the end state (thread = value row r)
+        const int quad = warp & 3, place = warp >> 2, r = 32 * quad + lane, h = NH == 2 ? r >> 6 : 0;
+        const uint32_t trow = tb + ((uint32_t)(32 * quad) << 16);
+        bool ok = true;
+        for (int c = 0; ok && c < chunks; ++c) {
+            const uint32_t par = c & 1, par2 = (c >> 1) & 1;
+            if (!(ok = wait_warp(&bars[X_FULL + par], par2, abort) && wait_warp(&bars[SC_FULL + par], par2, abort))) break;
+            const float *w = weights(c, h);
+#pragma unroll 1
+            for (int q = place; q < 4; q += 2) {
+                const int nq = 4 * c + q;
+                if (nq >= 2) {
+                    if (!(ok = wait_warp(&bars[W_FREE + place], (uint32_t)((nq >> 1) - 1) & 1, abort))) break;
+                    tc::tc_fence_after();
+                }
+                uint32_t acc = 0u;
+                const uint32_t xq = tc::smem_u32(sm + LY::x(par)) + 32 * 128 * q;
+                convert_w<TERMS, false>(trow, xq, w + 32 * q, place, quad, lane, acc);
+                if (__any_sync(0xffffffffu, saw_no_number(acc)))
+                    convert_w<TERMS, true>(trow, xq, w + 32 * q, place, quad, lane, acc);
+                if (q >= 2) arrive(SC_FREE + par);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                arrive(W_FULL + place);
+            }
+        }
+        if (ok && place == 0 && wait_warp(&bars[DONE], 0, abort) && (h == 0 || rw.two)) {
+            tc::tc_fence_after();
+            const long long srow = (long long)(rw.h0 + h) * p.dv + rw.r0 + (NH == 2 ? r & 63 : r);
+            float *dst = a.seg_state + (out * p.H * p.dv + srow) * DK;
+#pragma unroll 1
+            for (int k = 0; k < DK / 16; ++k) {
+                uint32_t v[16];
+                tc::tmem_ld16(trow + T_S + 16 * k, v);
+                tc::tmem_wait_ld();
+                store_row16(dst + 16 * k, v);
+            }
+            tc::tc_fence_before();
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------ loads, from the last chunk
+        if (lane == 0) {
+            tc::tma_prefetch_desc(&map_x);
+            tc::tma_prefetch_desc(&map_b);
+            int issued = 0;
+            for (int c = 0; c < chunks; ++c) {
+                const int k = c & 1, row = row0 + (chunks - 1 - c) * Q;
+                if (c >= 2 && !wait1(&bars[FREE + k], (uint32_t)((c >> 1) - 1) & 1, abort)) break;
+                tc::mbar_arrive_expect_tx(&bars[X_FULL + k], LY::XTILE);
+                for (int j = 0; j < R / 64; ++j)
+                    tc::tma_load_2d(sm + LY::x(k) + j * PANEL, &map_x, rw.col0 + 64 * j, row, &bars[X_FULL + k]);
+                tc::mbar_arrive_expect_tx(&bars[B_FULL + k], LY::CTILE);
+                for (int j = 0; j < LY::KP; ++j)
+                    tc::tma_load_2d(sm + LY::b(k) + j * PANEL, &map_b, rw.g * DK + 64 * j, row, &bars[B_FULL + k]);
+                ++issued;
+            }
+            for (int k = 0; k < 2; ++k) {
+                const int m = (issued + 1 - k) / 2;
+                if (m) {
+                    drain(&bars[B_FULL + k], (m - 1) & 1);
+                    drain(&bars[X_FULL + k], (m - 1) & 1);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------ products
+        if (lane == 0) {
+            constexpr uint32_t ID_S = tc::instr_desc(tc::FMT_BF16, false, true, R, DK);
+            constexpr uint64_t ROWS = 16 * 128 / 16;
+            bool ok = true;
+            for (int c = 0; ok && c < chunks; ++c) {
+                const uint32_t par = c & 1;
+                const uint64_t bd = tc::smem_desc(tc::smem_u32(sm + LY::b(par)), PANEL, 1024, tc::SWZ_128);
+                if (!(ok = wait1(&bars[B_FULL + par], (c >> 1) & 1, abort))) break;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    const int place = q & 1;
+                    if (!(ok = wait1(&bars[W_FULL + place], (uint32_t)q >> 1, abort))) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < TERMS; ++i)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            tc::mma_ts_f16(tb + T_S, tb + w_col(place, i) + 8 * k, bd + (2 * q + k) * ROWS, ID_S,
+                                           c + q + i + k > 0);
+                    tc::mma_commit(&bars[W_FREE + place]);
+                }
+                if (ok) tc::mma_commit(&bars[FREE + par]);  // (W of the chunk has been made, so x has been read too)
+            }
+            tc::mma_commit(&bars[DONE]);
+            if (!ok) drain(&bars[DONE], 0);
+        }
+        __syncwarp();
+    } else if (warp - 10 < NH) {
+        // ------------------------------------------------ weights of head h, from the last chunk
+        const int h = warp - 10;
+        const bool live = h == 0 || rw.two;
+        const float A = live ? in.A[rw.h0 + h] : 0.f, bias = live && in.dt_bias ? in.dt_bias[rw.h0 + h] : 0.f;
+        const int m = live ? Q : 0;
+        float behind = 0.f;
+        Steps st;
+        st.fetch(in, (long long)row0 + (chunks - 1) * Q, rw.h0 + h, lane, m);
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c) {
+            st.compute(bias, A, lane, m, behind);
+            behind += st.end;
+            st.fetch(in, (long long)row0 + (chunks - 2 - c) * Q, rw.h0 + h, lane, c + 1 < chunks ? m : 0);
+            if (c >= 2 && !(ok = wait_warp(&bars[SC_FREE + (c & 1)], (uint32_t)((c >> 1) - 1) & 1, abort))) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) weights(c, h)[32 * j + lane] = st.w[j];
+            arrive(SC_FULL + (c & 1));
+        }
+        if (ok && live && rw.r0 == 0 && lane == 0) a.seg_decay[out * p.H + rw.h0 + h] = behind;
+    }
+    __syncthreads();
+    if (warp == 9) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tb, T_COLS);
+    }
+}
+
+// Segments' own end states -> the states in front of them, in place: a thread
+// takes four elements of one sequence's state through its segments.
+template <class ST>
+__global__ void __launch_bounds__(256) ssm_join_kernel(const Args a, long long quads_per_seq) {
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    int seg = 0, s0, n;
+    const int i = seq_of_tile(a.q, (int)blockIdx.y, a.seg_len, seg, 0);
+    if (i < 0 || seg != 0 || id >= quads_per_seq) return;
+    const int slot = seq_slot(a.q, i);
+    if (!seq_range(a.q, i, s0, n) || slot < 0) return;
+    const int segs = segs_of(n, a.seg_len);
+    if (segs < 2) return;
+    const SsmParams &p = a.p;
+    const long long at = id * 4, per = quads_per_seq * 4;
+    const int h = (int)(at / ((long long)p.dv * p.dk));
+    const long long base = seg_base(s0, a.seg_len);
+    float s[4];
+    load_vec<4>(static_cast<const ST *>(p.S) + slot * per + at, s);
+    float4 *e = reinterpret_cast<float4 *>(a.seg_state + base * per + at);
+    const float *dec = a.seg_decay + base * p.H + h;
+    float4 next = *e;
+    for (int j = 0; j < segs; ++j, e += per / 4, dec += p.H) {
+        const float4 own = next;
+        if (j + 2 < segs) next = e[per / 4];
+        *e = make_float4(s[0], s[1], s[2], s[3]);
+        if (j + 1 == segs) break;
+        const float d = expf(*dec);
+        s[0] = fmaf(s[0], d, own.x);
+        s[1] = fmaf(s[1], d, own.y);
+        s[2] = fmaf(s[2], d, own.z);
+        s[3] = fmaf(s[3], d, own.w);
+    }
+}
+
+// A [rows, cols] bfloat16 matrix with a row stride, in boxes of box_rows rows of
+// box_cols columns (64 with 128-byte swizzle, 32 with 64-byte).
+cudaError_t row_map(CUtensorMap *m, const void *base, long long cols, long long rows, long long stride, int box_rows = Q, int box_cols = 64) {
     tc::EncodeTiledFn fn = tc::encoder();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)Q};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t es[2] = {1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <class ST, int DK, int NH>
-cudaError_t launch_typed(const SsmParams &p, const SeqIdx &q, cudaStream_t st) {
-    using LY = Layout<DK, NH>;
-    auto kern = ssm_tc_kernel<ST, DK, NH>;
+// Segment length of a call, or 0 (not split).
+int ssm_seg_len(int T, int n_seq, int H, int dv) {
+    return seg_len_for(T, n_seq, ((long long)H * dv + R - 1) / R, Q, SMS);
+}
+
+template <class ST, int DK, int NH, bool GATE>
+cudaError_t launch_typed(const SsmParams &p, const SeqIdx &q, void *work, cudaStream_t st) {
+    using LY = Layout<DK, NH, GATE>;
+    auto kern = ssm_tc_kernel<ST, DK, NH, GATE>;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), LY::REQUEST);
     if (e != cudaSuccess) return e;
-    CUtensorMap mx, mb, mc;
+    CUtensorMap mx, mb, mc, my, mz;
     const dl_ssm &in = p.in;
     if ((e = row_map(&mx, in.x, (long long)p.H * p.dv, q.T, in.x_stride)) != cudaSuccess) return e;
     if ((e = row_map(&mb, in.b, (long long)p.G * DK, q.T, in.b_stride)) != cudaSuccess) return e;
     if ((e = row_map(&mc, in.c, (long long)p.G * DK, q.T, in.c_stride)) != cudaSuccess) return e;
+    const long long yw = (long long)p.H * p.dv;
+    if ((e = row_map(&my, p.y, yw, q.T, yw, 32)) != cudaSuccess) return e;
+    mz = my;  // (not read without a gate)
+    if (GATE && (e = row_map(&mz, in.z, yw, q.T, in.z_stride, 32, 32)) != cudaSuccess) return e;
     const int per = p.H / p.G;
-    Args a{p, q, (q.T + Q - 1) / Q * Q, NH == 2 ? p.G * ((per + 1) / 2) : p.H * (p.dv / R), nullptr};
+    const long long state = (long long)p.H * p.dv * DK;  // of a sequence
+    int seg_len = ssm_seg_len(q.T, q.n_seq, p.H, p.dv);
+    float *ws = seg_len ? static_cast<float *>(work) : nullptr;
+    const bool split = seg_len != 0;
+    if (!split) seg_len = (int)std::min<long long>(((long long)q.T + Q - 1) / Q * Q, 0x7fffff80LL);
+    Args a{p, q, seg_len, NH == 2 ? p.G * ((per + 1) / 2) : p.H * (p.dv / R), ws,
+           split ? ws + seg_count(q.T, seg_len) * state : nullptr};
     const long long blocks = ((long long)q.T / a.seg_len + q.n_seq) * a.units;
-    kern<<<(unsigned)blocks, THREADS, LY::REQUEST, st>>>(mx, mb, mc, a);
+    if (split) {
+        using LE = EndLayout<DK, NH>;
+        auto ends = ssm_tc_ends_kernel<DK, NH>;
+        if ((e = allow_smem(reinterpret_cast<const void *>(ends), LE::REQUEST)) != cudaSuccess) return e;
+        const unsigned ends_max = (unsigned)(q.T / seg_len);  // segments with another behind them
+        ends<<<ends_max * (unsigned)a.units, END_THREADS, LE::REQUEST, st>>>(mx, mb, a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        ssm_join_kernel<ST><<<dim3((unsigned)((state / 4 + 255) / 256), ends_max), 256, 0, st>>>(a, state / 4);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    kern<<<(unsigned)blocks, THREADS, LY::REQUEST, st>>>(mx, mb, mc, my, mz, a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
+size_t ssm_work_bytes(int T, int n_seq, int H, int dk, int dv) {
+    const int len = ssm_seg_len(T, n_seq, H, dv);
+    return len ? (size_t)seg_count(T, len) * H * ((size_t)dv * dk + 1) * sizeof(float) : 0;
+}
+
 bool ssm_tc_supported(const SsmParams &p) { return p.in.dtype == DL_BF16 && tc::encoder() != nullptr; }
 
-cudaError_t launch_ssm_tc(const SsmParams &p, const SeqIdx &q, cudaStream_t st) {
+cudaError_t launch_ssm_tc(const SsmParams &p, const SeqIdx &q, void *work, cudaStream_t st) {
     auto with_nh = [&](auto s, auto dk) -> cudaError_t {
         using ST = decltype(s);
         constexpr int DK = decltype(dk)::value;
-        return p.dv == 64 ? launch_typed<ST, DK, 2>(p, q, st) : launch_typed<ST, DK, 1>(p, q, st);
+        if (p.in.z) return p.dv == 64 ? launch_typed<ST, DK, 2, true>(p, q, work, st) : launch_typed<ST, DK, 1, true>(p, q, work, st);
+        return p.dv == 64 ? launch_typed<ST, DK, 2, false>(p, q, work, st) : launch_typed<ST, DK, 1, false>(p, q, work, st);
     };
     auto with_dk = [&](auto s) -> cudaError_t {
         return p.dk == 64 ? with_nh(s, std::integral_constant<int, 64>{}) : with_nh(s, std::integral_constant<int, 128>{});

@@ -18,7 +18,7 @@ namespace stc {
 constexpr int Q = 128;        // tokens of a chunk: the rows of every token operand
 constexpr int R = 128;        // value rows of a block: one head's, or two heads' of 64
 constexpr int PANEL = Q * 128;  // 128 rows of 64 bf16 under 128-byte swizzle
-constexpr int THREADS = 512;
+constexpr int THREADS = 768;
 constexpr int SMEM_LIMIT = 227 * 1024;
 
 // Byte of (row, 16-byte piece) of a tile of 64-column panels.
@@ -26,39 +26,61 @@ DL_HD inline constexpr int tile_off(int row, int piece) {
     return (piece >> 3) * PANEL + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
-// Per chunk and head, from the step sizes (floats): the log decay from the
-// chunk's start through token t, l; u = exp(l at the end of its 32 tokens - l) dt;
+// Byte of (row, 16-byte piece) of a warp's gate block: 32 rows of 32 columns under 64-byte swizzle.
+DL_HD inline constexpr int gate_off(int row, int piece) { return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
+
+// Per chunk and head, from the step sizes (floats): the base-2 log decay from
+// the chunk's start through token t, l; u = 2^(l at the end of its 32 tokens - l) dt;
 // dt; w = exp(log decay behind the token, within the chunk) dt; l at the end of
-// each 32 tokens; exp of the whole chunk's.
+// each 32 tokens; exp of the whole chunk's log decay.
 struct Scal {
     static constexpr int L = 0, U = Q, DT = 2 * Q, W = 3 * Q, RB = 4 * Q, E = 4 * Q + 4, FLOATS = 4 * Q + 8;
 };
 
-template <int DK, int NH>
+template <int DK, int NH, bool GATE>
 struct Layout {
     static constexpr int KP = DK / 64;          // panels of b, c and the state
     static constexpr int CTILE = KP * PANEL, XTILE = (R / 64) * PANEL, STILE = KP * PANEL;
-    static constexpr int C = 0, B = C + CTILE, X = B + 2 * CTILE, S = X + 2 * XTILE, SCAL = S + STILE;
+    static constexpr int C = 0, B = C + CTILE, X = B + 2 * CTILE, S = X + 2 * XTILE, Z = S + STILE;
+    static constexpr int NZ = 3, ZBLOCK = 32 * 64;  // gate blocks in flight for each of 4 warps
+    static constexpr int SCAL = Z + (GATE ? 4 * NZ * ZBLOCK : 0);
     static constexpr int SCAL_BYTES = Scal::FLOATS * 4;                 // one head of one chunk
     static constexpr int NF = SCAL + 2 * NH * SCAL_BYTES;               // masks of rows with no number: [2][4 warps][4]
     static constexpr int BAR = NF + 2 * 16 * 4;
-    static constexpr int N_BAR = 25;
+    static constexpr int N_BAR = 39;
     static constexpr int TSLOT = BAR + 8 * N_BAR, ABORT = TSLOT + 4, BYTES = ABORT + 12;
     static constexpr int REQUEST = BYTES + 1024;  // the kernel aligns its base to 1024
     static_assert(REQUEST <= SMEM_LIMIT, "shared memory of a block");
     static_assert(SCAL_BYTES % 16 == 0 && NF % 16 == 0 && BAR % 8 == 0, "alignment");
     DL_HD static constexpr int b(int i) { return B + i * CTILE; }
     DL_HD static constexpr int x(int i) { return X + i * XTILE; }
+    DL_HD static constexpr int z(int warp, int i) { return Z + (warp * NZ + i) * ZBLOCK; }
+    DL_HD static constexpr int scal(int i, int h) { return SCAL + (i * NH + h) * SCAL_BYTES; }
+};
+
+// The kernel of segments' end states: b and x in two buffers, a chunk's weights.
+template <int DK, int NH>
+struct EndLayout {
+    static constexpr int KP = DK / 64, CTILE = KP * PANEL, XTILE = (R / 64) * PANEL;
+    static constexpr int B = 0, X = 2 * CTILE, SCAL = X + 2 * XTILE, SCAL_BYTES = Q * 4;
+    static constexpr int BAR = SCAL + 2 * NH * SCAL_BYTES, N_BAR = 15;
+    static constexpr int TSLOT = BAR + 8 * N_BAR, ABORT = TSLOT + 4, BYTES = ABORT + 12;
+    static constexpr int REQUEST = BYTES + 1024;
+    static_assert(REQUEST <= SMEM_LIMIT, "shared memory of a block");
+    DL_HD static constexpr int b(int i) { return B + i * CTILE; }
+    DL_HD static constexpr int x(int i) { return X + i * XTILE; }
     DL_HD static constexpr int scal(int i, int h) { return SCAL + (i * NH + h) * SCAL_BYTES; }
 };
 
 // Tensor-memory columns (fp32 words): the state [R x DK]; the scores C B^T
-// [Q x Q], overwritten 32 columns at a time by the decayed scores as bf16
-// pairs (of one or two heads); the outputs [Q x R]; the decayed addends
-// [R x Q] as bf16 pairs, high and low parts.
-constexpr int T_S = 0, T_G = 128, T_Y = 256, T_W = 384, T_WLO = 448, T_COLS = 512;
+// [Q x Q], overwritten 16 columns at a time by the decayed scores as bf16
+// pairs (8 columns of each of one or two heads); the outputs [Q x R]; the
+// decayed addends of 32 tokens [R x 32] as bf16 pairs in up to three parts of
+// 16 columns, in two places used in turn.
+constexpr int T_S = 0, T_G = 128, T_Y = 256, T_W = 384, T_COLS = 512;
+DL_HD inline constexpr int w_col(int place, int part) { return T_W + 64 * place + 16 * part; }
 // Columns of head h's decayed scores of tokens 16 k .. 16 k + 15.
-DL_HD inline constexpr int p_col(int k, int h) { return T_G + 32 * (k >> 1) + 16 * h + 8 * (k & 1); }
+DL_HD inline constexpr int p_col(int k, int h) { return T_G + 16 * k + 8 * h; }
 
 }  // namespace stc
 }  // namespace dl

@@ -45,6 +45,13 @@ def g():
     return g
 
 
+@pytest.fixture(autouse=True)
+def _no_wait_ran_out(request, g):
+    yield
+    if "ssm" in request.node.name or "layer" in request.node.name:
+        assert g.dl_device_faults(clear=True) == 0
+
+
 def gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 
@@ -282,6 +289,17 @@ def test_ssm_prompt_shapes_and_types(g, dk, dv, dtype, s_dtype):
                          ids=str)
 def test_ssm_prompt_lengths(g, lens, dtype):
     check_prompt(g, lens, 3, 1, 128, 64, dtype, F32, gate=len(lens) > 1, seed=sum(lens), first=len(lens) - 1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("s_dtype", [F32, BF16])
+@pytest.mark.parametrize("lens,H,G,dk,dv", [([2600], 2, 1, 128, 128), ([2600], 3, 1, 64, 64), ([3, 2300, 0, 1, 1025, 513, 512, 511], 1, 1, 128, 64),
+                                            ([1537, 700, 2048], 2, 2, 64, 256)], ids=str)
+def test_ssm_prompt_split_over_its_length(g, lens, H, G, dk, dv, s_dtype, dtype):
+    """Few heads and long sequences: segments run side by side from states formed first."""
+    if dtype == BF16:
+        assert g.dl_ssm_work_bytes(sum(lens) + 3, len(lens), H, dk, dv) > 0
+    check_prompt(g, lens, H, G, dk, dv, dtype, s_dtype, gate=dk == 64, seed=H + dv, decay=0.02)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])

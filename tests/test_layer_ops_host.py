@@ -182,13 +182,16 @@ def replay(tmp_path_factory):
 
 
 def tiles(exe, cases):
-    """[[(seq, first, last), ...], ...] of (T, len, seq_start) cases."""
+    """([(seq, first, last), ...], [(seq, first, last, place), ...], places) of each (T, len, seq_start): the tiles, those
+    that are not a sequence's last with their place in the workspace, and its places."""
     text = "".join(f"{len(s) - 1} {T} {n} {' '.join(map(str, s))}\n" for T, n, s in cases)
     out = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=300, check=True).stdout
-    got, line = [], []
+    got, line, all_ = [], [], None
     for row in out.splitlines():
-        if row == "end":
-            got.append(line)
+        if row == "ends":
+            all_, line = line, []
+        elif row.startswith("end"):
+            got.append((all_, line, int(row.split()[1])))
             line = []
         else:
             line.append(tuple(int(v) for v in row.split()))
@@ -206,10 +209,14 @@ def test_tiles_cover_every_row_of_every_sequence_once(replay):
         for n in lens:
             start.append(start[-1] + n)
         cases.append((start[-1] + rng.choice([0, 1, 77]), rng.choice([32, 64, 96, 512]), start))
-    for (T, n, start), got in zip(cases, tiles(replay, cases)):
+    for (T, n, start), (got, ends, places) in zip(cases, tiles(replay, cases)):
         want = [(i, r) for i in range(len(start) - 1) for r in range(start[i], start[i + 1])]
         assert sorted((i, r) for i, a, z in got for r in range(a, z)) == want
         assert all((a - start[i]) % n == 0 and z - a <= n for i, a, z in got)
+        assert [e[:3] for e in ends] == sorted(t for t in got if t[2] < start[t[0] + 1])
+        # a sequence's places: its tiles' in order, no two sequences' alike, all inside the workspace
+        used = [e[3] for e in ends] + [e[3] + 1 for e in ends if e[2] + n >= start[e[0] + 1]]
+        assert len(set(used)) == len(used) and all(0 <= u < places for u in used)
 
 
 def test_bad_sequence_bounds_never_leave_the_rows(replay):
@@ -217,6 +224,7 @@ def test_bad_sequence_bounds_never_leave_the_rows(replay):
     big = 2 ** 31 - 1
     cases = [(100, 32, [rng.choice([-big, -5, 0, 3, 50, 100, 101, 4000, big]) for _ in range(rng.randrange(2, 9))])
              for _ in range(1000)]
-    for (T, _, start), got in zip(cases, tiles(replay, cases)):
-        for i, a, z in got:
+    for (T, _, start), (got, ends, places) in zip(cases, tiles(replay, cases)):
+        for i, a, z in got + [e[:3] for e in ends]:
             assert 0 <= start[i] <= a < z <= start[i + 1] <= T
+        assert all(0 <= e[3] and e[3] + 1 < places for e in ends)
