@@ -23,12 +23,12 @@
 //
 // One block per (sequence, 128 value rows): one head's, or two heads' of 64
 // that share b and c. It walks the chunks in order with S in tensor memory:
-//   warps 0-3    P from G (thread = token row)
+//   warps 0-3, 16-19  P from G, then y: read Y, + D x, gate, store (thread =
+//                token row), half of the columns each
 //   warps 4-7    S: to bfloat16 for C S^T and scaled in place for the next
 //                update (thread = value row); then Y's scaling (thread = token)
 //   warps 8-15   W from X, 32 tokens at a time, two sets of four warps in turn
-//   warps 16-19  y: read Y, + D x, gate, store (thread = token row)
-//   warp 20      TMA: b and x two chunks ahead, c one
+//   warp 20      TMA: x two chunks ahead, b and c one
 //   warp 21      issues the products: G, W^T B by 32 tokens, C S^T between them, P X
 //   warps 22-23  step sizes and decays of a chunk (one head each), one ahead
 // Each product's time at d_k = 128 is 512 cycles of the tensor pipe, W^T B three
@@ -70,8 +70,8 @@ struct Args {
 };
 
 enum Bar {
-    C_FULL, C_FREE, B_FULL, B_FREE = B_FULL + 2, X_FULL = B_FREE + 2, X_FREE = X_FULL + 2, SC_FULL = X_FREE + 2,
-    SC_FREE = SC_FULL + 2, Z_FULL = SC_FREE + 2, W_FULL = Z_FULL + 12, W_FREE = W_FULL + 2, S_READY = W_FREE + 2, G_DONE, P_READY, Y2_DONE, YS_READY, Y_DONE, Y_FREE, ST_DONE,
+    C_FULL, C_FREE, B_FULL, B_FREE, X_FULL, X_FREE = X_FULL + 3, SC_FULL = X_FREE + 3,
+    SC_FREE = SC_FULL + 2, Z_FULL = SC_FREE + 2, W_FULL = Z_FULL + 24, W_FREE = W_FULL + 2, S_READY = W_FREE + 2, G_DONE, P_READY, Y2_DONE, YS_READY, Y_DONE, Y_FREE, ST_DONE,
     DRAIN, BARS
 };
 
@@ -127,8 +127,45 @@ __device__ __forceinline__ Rows rows_of(const SsmParams &p, int u) {
     }
 }
 
-// x where the mask's bits are set, else 0 (a select that the compiler does not turn into branches).
-__device__ __forceinline__ float keep(float x, uint32_t mask) { return __uint_as_float(__float_as_uint(x) & mask); }
+// Pairs of floats in 64-bit registers: one instruction for two products or sums
+// (what these warps issue bounds them).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return pair(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ uint64_t pair_bf(uint32_t w) { return pair(bf_lo(w), bf_hi(w)); }  // of a bfloat16 pair
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ void unpair(uint64_t p, uint32_t &a, uint32_t &b) { asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(p)); }
+__device__ __forceinline__ uint32_t pack_bf2(uint64_t p) {
+    float a, b;
+    unpair(p, a, b);
+    return dl::pack_bf2(a, b);
+}
+using dl::pack_bf2;
+// The lowest n bits of a word (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    uint32_t r;
+    asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(0xffffffffu), "r"(max(n, 0)));  // (shifts clamp at 32)
+    return ~r;
+}
+// 16 floats (bits) times f.
+__device__ __forceinline__ void scale16(uint32_t (&v)[16], float f) {
+    const uint64_t ff = pair(f, f);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) unpair(mul2(pair(v[j], v[j + 1]), ff), v[j], v[j + 1]);
+}
 
 // Four 8 x 8 tiles of 16-bit elements from shared memory, transposed.
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
@@ -171,21 +208,21 @@ __device__ __forceinline__ void convert_w(uint32_t trow, uint32_t xt, const floa
         for (int k = 0; k < 2; ++k) ldmatrix4_trans(xr[k], xt + tile_off(16 * k + mtok, mpiece + 2 * half));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // 8 tokens: this lane's pair of them
-            const float2 ws = *reinterpret_cast<const float2 *>(w + 8 * j + 2 * (lane & 3));
+            const uint64_t ws = *reinterpret_cast<const uint64_t *>(w + 8 * j + 2 * (lane & 3));
 #pragma unroll
             for (int q = 0; q < 2; ++q) {  // value rows lane / 4 and + 8
                 const uint32_t x = xr[j >> 1][2 * (j & 1) + q];
-                float f0 = bf_lo(x) * ws.x, f1 = bf_hi(x) * ws.y;
+                uint64_t f = mul2(pair_bf(x), ws);
 #pragma unroll
                 for (int i = 0; i < TERMS; ++i) {
-                    const uint32_t word = pack_bf2(f0, f1);
+                    const uint32_t word = pack_bf2(f);
                     part[i][2 * j + q] = word;
                     if (i == 0) watch(acc, word);
-                    f0 -= bf_lo(word);
-                    f1 -= bf_hi(word);
+                    if (i + 1 < TERMS) f = fma2(pair_bf(word), pair(-1.f, -1.f), f);
                     if constexpr (CLEAN) {
-                        if (!(fabsf(f0) <= 3.4e38f)) f0 = 0.f;
-                        if (!(fabsf(f1) <= 3.4e38f)) f1 = 0.f;
+                        float f0, f1;
+                        unpair(f, f0, f1);
+                        f = pair(fabsf(f0) <= 3.4e38f ? f0 : 0.f, fabsf(f1) <= 3.4e38f ? f1 : 0.f);
                     }
                 }
             }
@@ -211,8 +248,6 @@ __device__ __forceinline__ void store_row16(bf16 *p, const uint32_t (&v)[16]) {
     reinterpret_cast<uint4 *>(p)[1] = pack8(v + 8);
 }
 
-__device__ __noinline__ float softplus_call(float u) { return softplus_f(u); }
-
 // Step sizes and decays of a chunk of one head, by one warp: lane = token of each 32.
 struct Steps {
     float raw[4];  // dt_raw of tokens lane, 32 + lane, ..
@@ -229,7 +264,7 @@ struct Steps {
         float before = 0.f;  // log decay in front of the 32 tokens
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            dt[j] = 32 * j + lane < m ? softplus_call(raw[j] + bias) : 0.f;
+            dt[j] = 32 * j + lane < m ? softplus_f(raw[j] + bias) : 0.f;
             l[j] = w[j] = dt[j] * A;
         }
 #pragma unroll
@@ -309,7 +344,10 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + LY::BAR);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + LY::TSLOT);
     volatile int *abort = reinterpret_cast<volatile int *>(sm + LY::ABORT);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (from a shuffle, so that the compiler knows them alike in a warp: a product
+    // whose operands it must first move to uniform registers takes 120 cycles to
+    // issue instead of its 64)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const SsmParams &p = a.p;
     const dl_ssm &in = p.in;
 
@@ -330,9 +368,10 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     if (tid == 0) {
         auto init = [&](int b, int count) { tc::mbar_init(&bars[b], count); };
         for (int b = 0; b < BARS; ++b) init(b, 1);
-        for (int b : {(int)S_READY, (int)W_FULL, (int)W_FULL + 1, (int)P_READY, (int)YS_READY, (int)Y_FREE}) init(b, 4);
+        for (int b : {(int)S_READY, (int)W_FULL, (int)W_FULL + 1, (int)YS_READY}) init(b, 4);
+        for (int b : {(int)P_READY, (int)Y_FREE}) init(b, 8);
+        for (int k = 0; k < LY::NX; ++k) init(X_FREE + k, 8);
         for (int k = 0; k < 2; ++k) {
-            init(X_FREE + k, 4);
             init(SC_FULL + k, NH);
             init(SC_FREE + k, 20);
         }
@@ -345,24 +384,42 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tb = *tslot;
+    const uint32_t tb = __shfl_sync(0xffffffffu, *tslot, 0);
     auto scal = [&](int c, int h) { return reinterpret_cast<float *>(sm + LY::scal(c & 1, h)); };
     auto arrive = [&](int b) {  // once per warp, after every lane's writes
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars[b]);
     };
 
-    if (warp < 4) {
-        // ------------------------------------------------ P from G (thread = token row t)
-        const int quad = warp, t = 32 * quad + lane;
+    if (warp < 4 || (warp >= 16 && warp < 20)) {
+        // ------------------------------------------------ P from G, and y (thread = token row t), half of the columns
+        const int quad = warp & 3, half = warp >> 4, t = 32 * quad + lane;
         const uint32_t trow = tb + ((uint32_t)(32 * quad) << 16);
+        const int yh = rw.h0 + (NH == 2 ? half : 0), ycol = rw.r0 + (NH == 2 ? 0 : 64 * half);  // head and column of this half
+        const bool live = NH == 1 || half == 0 || rw.two;
+        const float D = in.D && live ? in.D[yh] : 0.f;
+        const uint64_t DD = pair(D, D);
+        // the gate of the warp's rows: blocks of 16 columns, four a chunk, three in flight
+        int nz = 0;
+        const int zslot = 4 * half + quad;
+        auto load_z = [&]() {
+            if (GATE && lane == 0 && nz < 4 * chunks) {
+                uint64_t *full = &bars[Z_FULL + 3 * zslot + nz % 3];
+                tc::mbar_arrive_expect_tx(full, LY::ZBLOCK);
+                tc::tma_load_2d(sm + LY::z(zslot, nz % 3), &map_z, rw.col0 + 64 * half + 16 * (nz & 3),
+                                row0 + (nz >> 2) * Q + 32 * quad, full);
+                ++nz;
+            }
+        };
+        if constexpr (GATE)
+            for (int k = 0; k < 3; ++k) load_z();
         for (int c = 0; c < chunks; ++c) {
             const uint32_t par = c & 1, par2 = (c >> 1) & 1;
             if (!wait_warp(&bars[SC_FULL + par], par2, abort)) break;
             if (!wait_warp(&bars[G_DONE], par, abort)) break;
             tc::tc_fence_after();
             uint32_t r0[16], r1[16];  // 16 columns each, one being loaded
-            tc::tmem_ld16(trow + T_G, r0);
+            tc::tmem_ld16(trow + T_G + 16 * half, r0);
             // P of tokens 16 k .. 16 k + 15 from their scores
             auto decayed = [&](int k, const uint32_t (&g)[16], bool diagonal) {
                 uint32_t pw[8];
@@ -372,41 +429,41 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     const float lt = sc[Scal::L + t];
                     if (!diagonal) {
                         const float v = exp2_fast(lt - sc[Scal::RB + (k >> 1)]);
+                        const uint64_t vv = pair(v, v);
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
-                            const float4 u = *reinterpret_cast<const float4 *>(sc + Scal::U + 16 * k + e);
-                            pw[e / 2] = pack_bf2(__uint_as_float(g[e]) * (u.x * v), __uint_as_float(g[e + 1]) * (u.y * v));
-                            pw[e / 2 + 1] = pack_bf2(__uint_as_float(g[e + 2]) * (u.z * v), __uint_as_float(g[e + 3]) * (u.w * v));
+                            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(sc + Scal::U + 16 * k + e);
+                            pw[e / 2] = pack_bf2(mul2(pair(g[e], g[e + 1]), mul2(u.x, vv)));
+                            pw[e / 2 + 1] = pack_bf2(mul2(pair(g[e + 2], g[e + 3]), mul2(u.y, vv)));
                         }
-                    } else {  // tokens up to t
-                        const int ahead = 16 * k - t - 1;
+                    } else {  // tokens up to t: those bits of the packed words
+                        const int upto = 16 * (t + 1 - 16 * k);
+                        const uint64_t ll = pair(lt, lt);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 l = *reinterpret_cast<const float4 *>(sc + Scal::L + 16 * k + e);
-                            const float4 d = *reinterpret_cast<const float4 *>(sc + Scal::DT + 16 * k + e);
-                            const float lv[4] = {l.x, l.y, l.z, l.w}, dv[4] = {d.x, d.y, d.z, d.w};
-                            float o[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                o[i] = keep(__uint_as_float(g[e + i]) * (exp2_fast(lt - lv[i]) * dv[i]), (uint32_t)((ahead + e + i) >> 31));
-                            pw[e / 2] = pack_bf2(o[0], o[1]);
-                            pw[e / 2 + 1] = pack_bf2(o[2], o[3]);
+                        for (int e = 0; e < 16; e += 2) {
+                            float x0, x1;
+                            unpair(fma2(*reinterpret_cast<const uint64_t *>(sc + Scal::L + 16 * k + e), pair(-1.f, -1.f), ll), x0, x1);
+                            const uint64_t f = mul2(pair(exp2_fast(x0), exp2_fast(x1)),
+                                                    *reinterpret_cast<const uint64_t *>(sc + Scal::DT + 16 * k + e));
+                            pw[e / 2] = pack_bf2(mul2(pair(g[e], g[e + 1]), f)) & low_bits(upto - 16 * e);
                         }
                     }
                     tc::tmem_st8(trow + p_col(k, h), pw);
                 }
             };
+            // (of each 32 tokens, the 16 of this half)
 #pragma unroll 1
-            for (int kb = 0; kb <= quad; ++kb) {  // 32 tokens s
+            for (int kb = 0; kb <= quad; kb += 2) {
                 tc::tmem_wait_ld();
-                tc::tmem_ld16(trow + T_G + 32 * kb + 16, r1);
-                decayed(2 * kb, r0, kb == quad);
+                if (kb < quad) tc::tmem_ld16(trow + T_G + 32 * kb + 32 + 16 * half, r1);
+                decayed(2 * kb + half, r0, kb == quad);
+                if (kb == quad) break;
                 tc::tmem_wait_ld();
-                if (kb < quad) tc::tmem_ld16(trow + T_G + 32 * kb + 32, r0);
-                decayed(2 * kb + 1, r1, kb == quad);
+                if (kb + 1 < quad) tc::tmem_ld16(trow + T_G + 32 * kb + 64 + 16 * half, r0);
+                decayed(2 * kb + 2 + half, r1, kb + 1 == quad);
             }
 #pragma unroll 1
-            for (int k = 2 * quad + 2; k < 8; ++k) {  // tokens behind every t of the warp
+            for (int k = 2 * quad + 2 + half; k < 8; k += 2) {  // tokens behind every t of the warp
                 uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int h = 0; h < NH; ++h) tc::tmem_st8(trow + p_col(k, h), zero);
@@ -414,7 +471,94 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             tc::tmem_wait_st();
             tc::tc_fence_before();
             arrive(P_READY);
+            if (c > 0) {  // the previous chunk's stores have read x's place: it may be loaded again
+                if (lane == 0) tc::bulk_wait_read<0>();
+                arrive(X_FREE + (c - 1) % LY::NX);
+            }
+
+            // y of row t: Y + D x, gated; through x's place in shared memory to
+            // HBM by TMA, or straight from registers where the warp's 32 rows
+            // reach behind the segment (or x holds what is no number)
+            const int m = min(Q, len - c * Q);
+            const long long row = (long long)row0 + c * Q + t;
+            if (!wait_warp(&bars[Y_DONE], par, abort)) break;
+            tc::tc_fence_after();
+            tc::tmem_ld16(trow + T_Y + 64 * half, r0);
+            const uint4 *nf = reinterpret_cast<const uint4 *>(sm + LY::NF) + 4 * (c % LY::NX);
+            uint32_t any = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) any |= nf[j].x | nf[j].y | nf[j].z | nf[j].w;
+            const bool direct = any || 32 * quad + 32 > m;
+            uint8_t *xp = sm + LY::x(c % LY::NX) + half * PANEL;
+            const uint32_t swz = (t & 7) << 4;
+            auto x_at = [&](int k, int j) {  // 8 of 16 value columns
+                return reinterpret_cast<uint4 *>(xp + t * 128 + ((32 * k + 16 * j) ^ swz));
+            };
+            auto columns = [&](auto direct_c) {
+                auto finish = [&](int k, const uint32_t (&y)[16], uint4 x0, uint4 x1) {
+                    const int zi = 4 * c + k;
+                    if (GATE && !wait_warp(&bars[Z_FULL + 3 * zslot + zi % 3], (zi / 3) & 1, abort)) return false;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 xv = j ? x1 : x0;
+                        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                        uint32_t zw[4] = {0u, 0u, 0u, 0u}, ow[4];
+                        if constexpr (GATE) {
+                            const uint4 zv = *reinterpret_cast<const uint4 *>(sm + LY::z(zslot, zi % 3) + gate_off(lane, j));
+                            zw[0] = zv.x, zw[1] = zv.y, zw[2] = zv.z, zw[3] = zv.w;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint64_t o = fma2(DD, pair_bf(xw[e]), pair(y[8 * j + 2 * e], y[8 * j + 2 * e + 1]));
+                            if constexpr (GATE) o = mul2(o, pair(silu_f<bf16>(bf_lo(zw[e])), silu_f<bf16>(bf_hi(zw[e]))));
+                            ow[e] = pack_bf2(o);
+                        }
+                        const uint4 out = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                        if constexpr (!decltype(direct_c)::value)
+                            *x_at(k, j) = out;
+                        else if (t < m && live)
+                            reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.y) + (row * p.H + yh) * p.dv + ycol)[2 * k + j] = out;
+                    }
+                    if constexpr (GATE) {
+                        __syncwarp();
+                        load_z();
+                    }
+                    return true;
+                };
+#pragma unroll 1
+                for (int k = 0; k < 4; k += 2) {  // 16 value columns each
+                    const uint4 xa = *x_at(k, 0), xb = *x_at(k, 1), xc = *x_at(k + 1, 0), xd = *x_at(k + 1, 1);
+                    tc::tmem_wait_ld();
+                    tc::tmem_ld16(trow + T_Y + 64 * half + 16 * k + 16, r1);
+                    if (!finish(k, r0, xa, xb)) return false;
+                    tc::tmem_wait_ld();
+                    if (k == 0) tc::tmem_ld16(trow + T_Y + 64 * half + 32, r0);
+                    if (!finish(k + 1, r1, xc, xd)) return false;
+                }
+                return true;
+            };
+            if (!(direct ? columns(std::true_type{}) : columns(std::false_type{}))) break;
+            tc::tc_fence_before();
+            arrive(Y_FREE);
+            if (!direct) {
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && live) {
+                    tc::tma_store_2d(&map_y, rw.col0 + 64 * half, row0 + c * Q + 32 * quad, xp + quad * 4096);
+                    tc::bulk_commit();
+                }
+            } else if (any && t < m && live) {
+                add_no_numbers(p, (long long)row0 + c * Q, t, reinterpret_cast<const uint32_t *>(nf), scal(c, NH == 2 ? half : 0), yh,
+                               rw.g, ycol, 64);
+            }
             arrive(SC_FREE + par);
+        }
+        if (lane == 0) {  // the warp's last copies have landed
+            tc::bulk_wait_all();
+            for (int k = 0; GATE && k < 3; ++k) {
+                const int n = (nz + 2 - k) / 3;
+                if (n) drain(&bars[Z_FULL + 3 * zslot + k], (n - 1) & 1);
+            }
         }
     } else if (warp < 8) {
         // ------------------------------------------------ S (thread = value row r), and Y's scaling (thread = token row r)
@@ -438,8 +582,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 uint8_t *dst = sm + LY::S + (k >> 2) * PANEL + r * 128;
                 *reinterpret_cast<uint4 *>(dst + (((32 * k) & 127) ^ ((r & 7) << 4))) = pack8(v);
                 *reinterpret_cast<uint4 *>(dst + (((32 * k + 16) & 127) ^ ((r & 7) << 4))) = pack8(v + 8);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * e);
+                scale16(v, e);
                 tc::tmem_st16(trow + T_S + 16 * k, v);
             };
             if (c == 0) {  // the state in front of the segment
@@ -483,9 +626,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             tc::tc_fence_after();
             tc::tmem_ld16(trow + T_Y, r0);
             auto scale = [&](int k, uint32_t (&v)[16]) {
-                const float f = NH == 2 && k >= 4 ? ex[NH - 1] : ex[0];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                scale16(v, NH == 2 && k >= 4 ? ex[NH - 1] : ex[0]);
                 tc::tmem_st16(trow + T_Y + 16 * k, v);
             };
 #pragma unroll 1
@@ -520,10 +661,11 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         for (int c = 0; c < chunks; ++c) {
             const uint32_t par = c & 1, par2 = (c >> 1) & 1;
             const int m = min(Q, len - c * Q);
-            uint8_t *xt = sm + LY::x(par);
-            if (!wait_warp(&bars[X_FULL + par], par2, abort)) break;
+            const int xi = c % LY::NX;
+            uint8_t *xt = sm + LY::x(xi);
+            if (!wait_warp(&bars[X_FULL + xi], (uint32_t)(c / LY::NX) & 1, abort)) break;
             if (!wait_warp(&bars[SC_FULL + par], par2, abort)) break;
-            if (m < Q && !wait_warp(&bars[B_FULL + par], par2, abort)) break;
+            if (m < Q && !wait_warp(&bars[B_FULL], par, abort)) break;
             const float *w = scal(c, h) + Scal::W;
             bool ok = true;
 #pragma unroll 1
@@ -533,7 +675,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     constexpr int BP = DK / 32;  // pieces of a row of b for each warp
                     for (int k = lane; k < 32 * (4 + BP); k += 32) {
                         const int row = 32 * q + k / (4 + BP), pc = k % (4 + BP);
-                        uint8_t *dst = pc < 4 ? xt + tile_off(row, 4 * quad + pc) : sm + LY::b(par) + tile_off(row, BP * quad + pc - 4);
+                        uint8_t *dst = pc < 4 ? xt + tile_off(row, 4 * quad + pc) : sm + LY::B + tile_off(row, BP * quad + pc - 4);
                         if (row >= m) *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     tc::fence_async_smem();
@@ -559,127 +701,13 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     mask = __reduce_or_sync(0xffffffffu, mask);
                     tc::fence_async_smem();
                 }
-                if (lane == 0) nf[16 * par + q] = mask;
+                if (lane == 0) nf[16 * xi + q] = mask;
                 if (q >= 2) arrive(SC_FREE + par);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 arrive(W_FULL + place);
             }
             if (!ok) break;
-        }
-    } else if (warp >= 16 && warp < 20) {
-        // ------------------------------------------------ y (thread = token row t)
-        const int quad = warp & 3, t = 32 * quad + lane;
-        const uint32_t trow = tb + ((uint32_t)(32 * quad) << 16);
-        float D[NH];
-#pragma unroll
-        for (int h = 0; h < NH; ++h) D[h] = in.D && (h == 0 || rw.two) ? in.D[rw.h0 + h] : 0.f;
-        // the gate of the warp's rows: blocks of 32 columns, four a chunk, three in flight
-        int nz = 0;
-        auto load_z = [&]() {
-            if (GATE && lane == 0 && nz < 4 * chunks) {
-                uint64_t *full = &bars[Z_FULL + 3 * quad + nz % 3];
-                tc::mbar_arrive_expect_tx(full, LY::ZBLOCK);
-                tc::tma_load_2d(sm + LY::z(quad, nz % 3), &map_z, rw.col0 + 32 * (nz & 3), row0 + (nz >> 2) * Q + 32 * quad, full);
-                ++nz;
-            }
-        };
-        if constexpr (GATE)
-            for (int k = 0; k < 3; ++k) load_z();
-        for (int c = 0; c < chunks; ++c) {
-            const uint32_t par = c & 1;
-            if (c > 0) {  // the previous chunk's stores have read x's place: it may be loaded again
-                if (lane == 0) tc::bulk_wait_read<0>();
-                arrive(X_FREE + (par ^ 1));
-            }
-
-            // y of row t: Y + D x, gated; through x's place in shared memory to
-            // HBM by TMA, or straight from registers where the warp's 32 rows
-            // reach behind the segment (or x holds what is no number)
-            const int m = min(Q, len - c * Q);
-            const long long row = (long long)row0 + c * Q + t;
-            if (!wait_warp(&bars[Y_DONE], par, abort)) break;
-            tc::tc_fence_after();
-            const uint4 *nf = reinterpret_cast<const uint4 *>(sm + LY::NF) + 4 * par;
-            uint32_t any = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) any |= nf[j].x | nf[j].y | nf[j].z | nf[j].w;
-            const bool direct = any || 32 * quad + 32 > m;
-            uint8_t *xt = sm + LY::x(par);
-            uint32_t r0[16], r1[16];  // 16 columns each, one being loaded
-            tc::tmem_ld16(trow + T_Y, r0);
-            uint8_t *xrow = xt + t * 128;
-            const uint32_t swz = (t & 7) << 4;
-            auto x_at = [&](int k, int j) {  // 8 of 16 value columns
-                return reinterpret_cast<uint4 *>(xrow + (k >> 2) * PANEL + (((32 * k + 16 * j) & 127) ^ swz));
-            };
-            auto columns = [&](auto direct_c) {
-                auto finish = [&](int k, const uint32_t (&y)[16], uint4 x0, uint4 x1, const uint8_t *zrow) {
-                    const int h = NH == 2 ? k >> 2 : 0;
-                    const float d = h ? D[NH - 1] : D[0];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float x[8], o[8];
-                        StateVec<bf16>::unpack(j ? x1 : x0, x);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = fmaf(d, x[e], __uint_as_float(y[8 * j + e]));
-                        if constexpr (GATE) {
-                            float z[8];
-                            StateVec<bf16>::unpack(*reinterpret_cast<const uint4 *>(zrow + gate_off(lane, 2 * (k & 1) + j)), z);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] *= silu_f<bf16>(z[e]);
-                        }
-                        const uint4 out = StateVec<bf16>::pack(o);
-                        if constexpr (!decltype(direct_c)::value)
-                            *x_at(k, j) = out;
-                        else if (t < m && (h == 0 || rw.two))
-                            reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.y) + row * p.H * p.dv + rw.col0)[2 * k + j] = out;
-                    }
-                };
-#pragma unroll 1
-                for (int cb = 0; cb < 4; ++cb) {  // 32 value columns
-                    const int zi = 4 * c + cb;
-                    const uint4 xa = *x_at(2 * cb, 0), xb = *x_at(2 * cb, 1), xc = *x_at(2 * cb + 1, 0), xd = *x_at(2 * cb + 1, 1);
-                    if (GATE && !wait_warp(&bars[Z_FULL + 3 * quad + zi % 3], (zi / 3) & 1, abort)) return false;
-                    const uint8_t *zrow = sm + LY::z(quad, GATE ? zi % 3 : 0);
-                    tc::tmem_wait_ld();
-                    tc::tmem_ld16(trow + T_Y + 32 * cb + 16, r1);
-                    finish(2 * cb, r0, xa, xb, zrow);
-                    tc::tmem_wait_ld();
-                    if (cb < 3) tc::tmem_ld16(trow + T_Y + 32 * cb + 32, r0);
-                    finish(2 * cb + 1, r1, xc, xd, zrow);
-                    if constexpr (GATE) {
-                        __syncwarp();
-                        load_z();
-                    }
-                }
-                return true;
-            };
-            if (!(direct ? columns(std::true_type{}) : columns(std::false_type{}))) break;
-            tc::tc_fence_before();
-            arrive(Y_FREE);
-            if (!direct) {
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    for (int k = 0; k < (NH == 2 && !rw.two ? 1 : R / 64); ++k)
-                        tc::tma_store_2d(&map_y, rw.col0 + 64 * k, row0 + c * Q + 32 * quad, xt + k * PANEL + quad * 4096);
-                    tc::bulk_commit();
-                }
-            } else if (any && t < m) {
-                for (int h = 0; h < NH; ++h)
-                    if (h == 0 || rw.two)
-                        add_no_numbers(p, (long long)row0 + c * Q, t, reinterpret_cast<const uint32_t *>(nf), scal(c, h), rw.h0 + h,
-                                       rw.g, rw.r0, R / NH);
-            }
-            arrive(SC_FREE + par);
-        }
-        if (lane == 0) {  // the warp's last copies have landed
-            tc::bulk_wait_all();
-            for (int k = 0; GATE && k < 3; ++k) {
-                const int n = (nz + 2 - k) / 3;
-                if (n) drain(&bars[Z_FULL + 3 * quad + k], (n - 1) & 1);
-            }
         }
     } else if (warp == 20) {
         // ------------------------------------------------ loads
@@ -692,37 +720,38 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 for (int k = 0; k < panels; ++k) tc::tma_load_2d(sm + off + k * PANEL, map, col + 64 * k, row, full);
             };
             int nb = 0, nx = 0, nc = 0;  // copies issued
-            for (int c = 0; c < chunks; ++c) {
-                const int k = c & 1, row = row0 + c * Q;
-                const uint32_t old = (uint32_t)((c >> 1) - 1) & 1;
-                if (c >= 2 && !wait1(&bars[B_FREE + k], old, abort)) break;
-                load(&map_b, LY::b(k), LY::KP, rw.g * DK, row, &bars[B_FULL + k]);
-                ++nb;
-                if (c == 0) {
-                    load(&map_c, LY::C, LY::KP, rw.g * DK, row, &bars[C_FULL]);
-                    ++nc;
-                }
-                if (c >= 2 && !wait1(&bars[X_FREE + k], old, abort)) break;
-                load(&map_x, LY::x(k), R / 64, rw.col0, row, &bars[X_FULL + k]);
+            auto load_b = [&]() { load(&map_b, LY::B, LY::KP, rw.g * DK, row0 + nb++ * Q, &bars[B_FULL]); };
+            auto load_c = [&]() { load(&map_c, LY::C, LY::KP, rw.g * DK, row0 + nc++ * Q, &bars[C_FULL]); };
+            auto load_x = [&]() {
+                load(&map_x, LY::x(nx % LY::NX), R / 64, rw.col0, row0 + nx * Q, &bars[X_FULL + nx % LY::NX]);
                 ++nx;
-                if (c > 0) {
-                    if (!wait1(&bars[C_FREE], (c - 1) & 1, abort)) break;
-                    load(&map_c, LY::C, LY::KP, rw.g * DK, row, &bars[C_FULL]);
-                    ++nc;
+            };
+            load_b();
+            load_x();
+            load_c();
+            if (chunks > 1) load_x();
+            for (int c = 0; c + 1 < chunks; ++c) {  // in the order in which the places become free
+                if (c + 2 < chunks) {
+                    if (c > 0 && !wait1(&bars[X_FREE + (c - 1) % LY::NX], (uint32_t)((c - 1) / LY::NX) & 1, abort)) break;
+                    load_x();
                 }
+                if (!wait1(&bars[C_FREE], c & 1, abort)) break;
+                load_c();
+                if (!wait1(&bars[B_FREE], c & 1, abort)) break;
+                load_b();
             }
             // every copy has landed before the block may leave
-            for (int k = 0; k < 2; ++k) {
-                const int b = (nb + 1 - k) / 2, x = (nx + 1 - k) / 2;  // copies into buffer k
-                if (b) drain(&bars[B_FULL + k], (b - 1) & 1);
+            drain(&bars[B_FULL], (nb - 1) & 1);
+            drain(&bars[C_FULL], (nc - 1) & 1);
+            for (int k = 0; k < LY::NX; ++k) {
+                const int x = (nx + LY::NX - 1 - k) / LY::NX;  // copies into place k
                 if (x) drain(&bars[X_FULL + k], (x - 1) & 1);
             }
-            if (nc) drain(&bars[C_FULL], (nc - 1) & 1);
         }
         __syncwarp();
     } else if (warp == 21) {
         // ------------------------------------------------ products
-        if (lane == 0) {
+        if (tc::elect_one()) {
             constexpr uint32_t ID_G = tc::instr_desc(tc::FMT_BF16, false, false, Q, Q);
             constexpr uint32_t ID_Y2 = tc::instr_desc(tc::FMT_BF16, false, false, Q, R);
             constexpr uint32_t ID_Y1 = tc::instr_desc(tc::FMT_BF16, false, true, Q, R / NH);
@@ -735,11 +764,10 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             auto nmajor = [&](int off) { return tc::smem_desc(tc::smem_u32(sm + off), PANEL, 1024, tc::SWZ_128); };
             constexpr uint64_t COLS = 32 / 16, PANELS = PANEL / 16, ROWS = 16 * 128 / 16;
             const uint64_t ck = kmajor(LY::C), sk = kmajor(LY::S);
-            const uint64_t bk[2] = {kmajor(LY::b(0)), kmajor(LY::b(1))}, bn[2] = {nmajor(LY::b(0)), nmajor(LY::b(1))},
-                           xn[2] = {nmajor(LY::x(0)), nmajor(LY::x(1))};
+            const uint64_t bk = kmajor(LY::B), bn = nmajor(LY::B), xn = nmajor(LY::X);
             bool ok = true;
             for (int c = 0; c < chunks; ++c) {
-                const uint32_t par = c & 1, par2 = (c >> 1) & 1;
+                const uint32_t par = c & 1;
                 // A B^T over DK columns of two tiles
                 auto over_columns = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t id) {
 #pragma unroll
@@ -750,7 +778,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 };
                 // S' of 64 tokens
                 auto update = [&](int half) {
-                    const uint64_t bd = (par ? bn[1] : bn[0]) + half * 4 * ROWS;
+                    const uint64_t bd = bn + half * 4 * ROWS;
 #pragma unroll
                     for (int place = 0; place < 2; ++place) {
                         if (!wait1(&bars[W_FULL + place], (uint32_t)half, abort)) return false;  // (two uses a chunk)
@@ -764,9 +792,9 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     }
                     return true;
                 };
-                if (!(ok = wait1(&bars[C_FULL], par, abort) && wait1(&bars[B_FULL + par], par2, abort))) break;
+                if (!(ok = wait1(&bars[C_FULL], par, abort) && wait1(&bars[B_FULL], par, abort))) break;
                 tc::tc_fence_after();
-                over_columns(tb + T_G, ck, par ? bk[1] : bk[0], ID_G);
+                over_columns(tb + T_G, ck, bk, ID_G);
                 tc::mma_commit(&bars[G_DONE]);
                 if (!(ok = wait1(&bars[S_READY], par, abort) && update(0))) break;
                 if (!(ok = c == 0 || wait1(&bars[Y_FREE], (c - 1) & 1, abort))) break;
@@ -776,10 +804,10 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 tc::mma_commit(&bars[C_FREE]);
                 if (!(ok = update(1))) break;
                 tc::mma_commit(&bars[ST_DONE]);
-                tc::mma_commit(&bars[B_FREE + par]);
+                tc::mma_commit(&bars[B_FREE]);
                 if (!(ok = wait1(&bars[P_READY], par, abort) && wait1(&bars[YS_READY], par, abort))) break;
                 tc::tc_fence_after();
-                const uint64_t xd = par ? xn[1] : xn[0];
+                const uint64_t xd = xn + (c % LY::NX) * (LY::XTILE / 16);
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -793,7 +821,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             }
         }
         __syncwarp();
-    } else if (warp - 22 < NH) {
+    } else if (warp >= 22 && warp < 22 + NH) {
         // ------------------------------------------------ step sizes and decays of head h
         const int h = warp - 22;
         const bool live = h == 0 || rw.two;
@@ -830,14 +858,17 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     using LY = EndLayout<DK, NH>;
     constexpr int TERMS = 3;
     enum { B_FULL, FREE = B_FULL + 2, X_FULL = FREE + 2, SC_FULL = X_FULL + 2, SC_FREE = SC_FULL + 2, W_FULL = SC_FREE + 2,
-           W_FREE = W_FULL + 2, DONE = W_FREE + 2, BARS };
+           W_FREE = W_FULL + 4, DONE = W_FREE + 4, BARS };  // (a place of W for each 32 tokens of a chunk)
     static_assert(LY::N_BAR == BARS, "barriers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + LY::BAR);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + LY::TSLOT);
     volatile int *abort = reinterpret_cast<volatile int *>(sm + LY::ABORT);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (from a shuffle, so that the compiler knows them alike in a warp: a product
+    // whose operands it must first move to uniform registers takes 120 cycles to
+    // issue instead of its 64)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const SsmParams &p = a.p;
     const dl_ssm &in = p.in;
 
@@ -864,7 +895,7 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     }
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tb = *tslot;
+    const uint32_t tb = __shfl_sync(0xffffffffu, *tslot, 0);
     auto weights = [&](int c, int h) { return reinterpret_cast<float *>(sm + LY::scal(c & 1, h)); };
     auto arrive = [&](int b) {
         __syncwarp();
@@ -873,7 +904,7 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
 
     if (warp < 8) {
         // ------------------------------------------------ W, every other 32 tokens; the end state (thread = value row r)
-        const int quad = warp & 3, place = warp >> 2, r = 32 * quad + lane, h = NH == 2 ? r >> 6 : 0;
+        const int quad = warp & 3, set = warp >> 2, r = 32 * quad + lane, h = NH == 2 ? r >> 6 : 0;
         const uint32_t trow = tb + ((uint32_t)(32 * quad) << 16);
         bool ok = true;
         for (int c = 0; ok && c < chunks; ++c) {
@@ -881,24 +912,23 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (!(ok = wait_warp(&bars[X_FULL + par], par2, abort) && wait_warp(&bars[SC_FULL + par], par2, abort))) break;
             const float *w = weights(c, h);
 #pragma unroll 1
-            for (int q = place; q < 4; q += 2) {
-                const int nq = 4 * c + q;
-                if (nq >= 2) {
-                    if (!(ok = wait_warp(&bars[W_FREE + place], (uint32_t)((nq >> 1) - 1) & 1, abort))) break;
+            for (int q = set; q < 4; q += 2) {
+                if (c > 0) {
+                    if (!(ok = wait_warp(&bars[W_FREE + q], (uint32_t)(c - 1) & 1, abort))) break;
                     tc::tc_fence_after();
                 }
                 uint32_t acc = 0u;
                 const uint32_t xq = tc::smem_u32(sm + LY::x(par)) + 32 * 128 * q;
-                convert_w<TERMS, false>(trow, xq, w + 32 * q, place, quad, lane, acc);
+                convert_w<TERMS, false>(trow, xq, w + 32 * q, q - 2, quad, lane, acc);
                 if (__any_sync(0xffffffffu, saw_no_number(acc)))
-                    convert_w<TERMS, true>(trow, xq, w + 32 * q, place, quad, lane, acc);
+                    convert_w<TERMS, true>(trow, xq, w + 32 * q, q - 2, quad, lane, acc);
                 if (q >= 2) arrive(SC_FREE + par);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
-                arrive(W_FULL + place);
+                arrive(W_FULL + q);
             }
         }
-        if (ok && place == 0 && wait_warp(&bars[DONE], 0, abort) && (h == 0 || rw.two)) {
+        if (ok && set == 0 && wait_warp(&bars[DONE], 0, abort) && (h == 0 || rw.two)) {
             tc::tc_fence_after();
             const long long srow = (long long)(rw.h0 + h) * p.dv + rw.r0 + (NH == 2 ? r & 63 : r);
             float *dst = a.seg_state + (out * p.H * p.dv + srow) * DK;
@@ -939,7 +969,7 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         __syncwarp();
     } else if (warp == 9) {
         // ------------------------------------------------ products
-        if (lane == 0) {
+        if (tc::elect_one()) {
             constexpr uint32_t ID_S = tc::instr_desc(tc::FMT_BF16, false, true, R, DK);
             constexpr uint64_t ROWS = 16 * 128 / 16;
             bool ok = true;
@@ -949,16 +979,15 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                 if (!(ok = wait1(&bars[B_FULL + par], (c >> 1) & 1, abort))) break;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
-                    const int place = q & 1;
-                    if (!(ok = wait1(&bars[W_FULL + place], (uint32_t)q >> 1, abort))) break;
+                    if (!(ok = wait1(&bars[W_FULL + q], par, abort))) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < TERMS; ++i)
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            tc::mma_ts_f16(tb + T_S, tb + w_col(place, i) + 8 * k, bd + (2 * q + k) * ROWS, ID_S,
+                            tc::mma_ts_f16(tb + T_S, tb + w_col(q - 2, i) + 8 * k, bd + (2 * q + k) * ROWS, ID_S,
                                            c + q + i + k > 0);
-                    tc::mma_commit(&bars[W_FREE + place]);
+                    tc::mma_commit(&bars[W_FREE + q]);
                 }
                 if (ok) tc::mma_commit(&bars[FREE + par]);  // (W of the chunk has been made, so x has been read too)
             }
@@ -1029,7 +1058,7 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const Args a, long long q
 }
 
 // A [rows, cols] bfloat16 matrix with a row stride, in boxes of box_rows rows of
-// box_cols columns (64 with 128-byte swizzle, 32 with 64-byte).
+// box_cols columns (64 with 128-byte swizzle, 16 with 32-byte).
 cudaError_t row_map(CUtensorMap *m, const void *base, long long cols, long long rows, long long stride, int box_rows = Q, int box_cols = 64) {
     tc::EncodeTiledFn fn = tc::encoder();
     if (!fn) return cudaErrorNotSupported;
@@ -1038,7 +1067,7 @@ cudaError_t row_map(CUtensorMap *m, const void *base, long long cols, long long 
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t es[2] = {1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_32B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -1063,7 +1092,7 @@ cudaError_t launch_typed(const SsmParams &p, const SeqIdx &q, void *work, cudaSt
     const long long yw = (long long)p.H * p.dv;
     if ((e = row_map(&my, p.y, yw, q.T, yw, 32)) != cudaSuccess) return e;
     mz = my;  // (not read without a gate)
-    if (GATE && (e = row_map(&mz, in.z, yw, q.T, in.z_stride, 32, 32)) != cudaSuccess) return e;
+    if (GATE && (e = row_map(&mz, in.z, yw, q.T, in.z_stride, 32, 16)) != cudaSuccess) return e;
     const int per = p.H / p.G;
     const long long state = (long long)p.H * p.dv * DK;  // of a sequence
     int seg_len = ssm_seg_len(q.T, q.n_seq, p.H, p.dv);

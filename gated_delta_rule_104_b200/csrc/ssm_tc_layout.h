@@ -26,8 +26,8 @@ DL_HD inline constexpr int tile_off(int row, int piece) {
     return (piece >> 3) * PANEL + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
-// Byte of (row, 16-byte piece) of a warp's gate block: 32 rows of 32 columns under 64-byte swizzle.
-DL_HD inline constexpr int gate_off(int row, int piece) { return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
+// Byte of (row, 16-byte piece) of a warp's gate block: 32 rows of 16 columns under 32-byte swizzle.
+DL_HD inline constexpr int gate_off(int row, int piece) { return row * 32 + ((piece ^ ((row >> 2) & 1)) << 4); }
 
 // Per chunk and head, from the step sizes (floats): the base-2 log decay from
 // the chunk's start through token t, l; u = 2^(l at the end of its 32 tokens - l) dt;
@@ -41,18 +41,18 @@ template <int DK, int NH, bool GATE>
 struct Layout {
     static constexpr int KP = DK / 64;          // panels of b, c and the state
     static constexpr int CTILE = KP * PANEL, XTILE = (R / 64) * PANEL, STILE = KP * PANEL;
-    static constexpr int C = 0, B = C + CTILE, X = B + 2 * CTILE, S = X + 2 * XTILE, Z = S + STILE;
-    static constexpr int NZ = 3, ZBLOCK = 32 * 64;  // gate blocks in flight for each of 4 warps
-    static constexpr int SCAL = Z + (GATE ? 4 * NZ * ZBLOCK : 0);
+    static constexpr int NX = 3;  // chunks of x in flight
+    static constexpr int C = 0, B = C + CTILE, X = B + CTILE, S = X + NX * XTILE, Z = S + STILE;
+    static constexpr int NZ = 3, ZBLOCK = 32 * 32;  // gate blocks in flight for each of 8 warps
+    static constexpr int SCAL = Z + (GATE ? 8 * NZ * ZBLOCK : 0);
     static constexpr int SCAL_BYTES = Scal::FLOATS * 4;                 // one head of one chunk
-    static constexpr int NF = SCAL + 2 * NH * SCAL_BYTES;               // masks of rows with no number: [2][4 warps][4]
-    static constexpr int BAR = NF + 2 * 16 * 4;
-    static constexpr int N_BAR = 39;
+    static constexpr int NF = SCAL + 2 * NH * SCAL_BYTES;               // masks of rows with no number: [NX][4 warps][4]
+    static constexpr int BAR = NF + NX * 16 * 4;
+    static constexpr int N_BAR = 51;
     static constexpr int TSLOT = BAR + 8 * N_BAR, ABORT = TSLOT + 4, BYTES = ABORT + 12;
     static constexpr int REQUEST = BYTES + 1024;  // the kernel aligns its base to 1024
     static_assert(REQUEST <= SMEM_LIMIT, "shared memory of a block");
     static_assert(SCAL_BYTES % 16 == 0 && NF % 16 == 0 && BAR % 8 == 0, "alignment");
-    DL_HD static constexpr int b(int i) { return B + i * CTILE; }
     DL_HD static constexpr int x(int i) { return X + i * XTILE; }
     DL_HD static constexpr int z(int warp, int i) { return Z + (warp * NZ + i) * ZBLOCK; }
     DL_HD static constexpr int scal(int i, int h) { return SCAL + (i * NH + h) * SCAL_BYTES; }
@@ -63,7 +63,7 @@ template <int DK, int NH>
 struct EndLayout {
     static constexpr int KP = DK / 64, CTILE = KP * PANEL, XTILE = (R / 64) * PANEL;
     static constexpr int B = 0, X = 2 * CTILE, SCAL = X + 2 * XTILE, SCAL_BYTES = Q * 4;
-    static constexpr int BAR = SCAL + 2 * NH * SCAL_BYTES, N_BAR = 15;
+    static constexpr int BAR = SCAL + 2 * NH * SCAL_BYTES, N_BAR = 19;
     static constexpr int TSLOT = BAR + 8 * N_BAR, ABORT = TSLOT + 4, BYTES = ABORT + 12;
     static constexpr int REQUEST = BYTES + 1024;
     static_assert(REQUEST <= SMEM_LIMIT, "shared memory of a block");
@@ -76,7 +76,8 @@ struct EndLayout {
 // [Q x Q], overwritten 16 columns at a time by the decayed scores as bf16
 // pairs (8 columns of each of one or two heads); the outputs [Q x R]; the
 // decayed addends of 32 tokens [R x 32] as bf16 pairs in up to three parts of
-// 16 columns, in two places used in turn.
+// 16 columns, in two places used in turn (the kernel of end states, which has
+// neither scores nor outputs, uses two more in front of them: -2 and -1).
 constexpr int T_S = 0, T_G = 128, T_Y = 256, T_W = 384, T_COLS = 512;
 DL_HD inline constexpr int w_col(int place, int part) { return T_W + 64 * place + 16 * part; }
 // Columns of head h's decayed scores of tokens 16 k .. 16 k + 15.
