@@ -70,9 +70,9 @@ struct Args {
 };
 
 enum Bar {
-    C_FULL, C_FREE, B_FULL, B_FREE, X_FULL, X_FREE = X_FULL + 3, SC_FULL = X_FREE + 3,
-    SC_FREE = SC_FULL + 2, Z_FULL = SC_FREE + 2, W_FULL = Z_FULL + 24, W_FREE = W_FULL + 2, S_READY = W_FREE + 2, G_DONE, P_READY, Y2_DONE, YS_READY, Y_DONE, Y_FREE, ST_DONE,
-    DRAIN, BARS
+    C_FULL, C_FREE, B_FULL, B_FREE = B_FULL + 2, SC_FULL = B_FREE + 2,
+    SC_FREE = SC_FULL + 2, Z_FULL = SC_FREE + 2, W_FULL = Z_FULL + 24, W_FREE = W_FULL + W_PLACES, S_READY = W_FREE + W_PLACES, G_DONE, P_READY, Y2_DONE, YS_READY, Y_DONE, Y_FREE, ST_DONE,
+    DRAIN, X_FULL  // (then x's places' X_FREE)
 };
 
 __device__ __forceinline__ uint64_t globaltimer() {
@@ -174,11 +174,11 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                  : "r"(addr)
                  : "memory");
 }
-// 16 lanes x 16 columns: register 2 n holds lane (thread / 4), column 4 n + thread % 4,
+// 16 lanes x 8 columns: register 2 n holds lane (thread / 4), column 4 n + thread % 4,
 // register 2 n + 1 the same of lane + 8.
-__device__ __forceinline__ void tmem_st_16x16(uint32_t addr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void tmem_st_16x8(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
                  : "memory");
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -192,27 +192,29 @@ __device__ __forceinline__ void watch(uint32_t &acc, uint32_t pair) {
 }
 __device__ __forceinline__ bool saw_no_number(uint32_t acc) { return (acc & 0x7fff7fffu) != 0; }
 
-// W of a warp's 32 value rows and 32 tokens into a place of tensor memory, 16
-// rows and 16 tokens at a time: x tile xt (from the first of the tokens), their
-// weights w. Each of the TERMS parts holds the leading 8 bits of what the parts
-// before it leave; CLEAN drops parts behind the first that are no finite numbers.
+// W of a warp's 32 value rows and 16 tokens to tensor memory at `at`: x from its
+// rows of a quarter (xt: the first of the tokens), the tokens' weights w. Each of
+// the TERMS parts, 8 columns, holds the leading 8 bits of what the parts before
+// it leave; CLEAN drops parts behind the first that are no finite numbers.
 template <int TERMS, bool CLEAN>
-__device__ __forceinline__ void convert_w(uint32_t trow, uint32_t xt, const float *w, int place, int quad, int lane, uint32_t &acc) {
-    // this lane's row of the transposing loads: token (lane & 7) + 8 (lane >> 4) of
-    // 16, 8 value rows (lane >> 3) & 1 of 16
+__device__ __forceinline__ void convert_w(uint32_t at, uint32_t xt, const float *w, int quad, int lane, uint32_t &acc) {
+    // this lane's row of the transposing loads: token (lane & 7) + 8 (lane >> 4),
+    // 8 value rows (lane >> 3) & 1 of 16
     const int mtok = (lane & 7) + ((lane >> 4) << 3), mpiece = 4 * quad + ((lane >> 3) & 1);
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {  // 16 value rows
-        uint32_t xr[2][4], part[TERMS][8];
+    uint32_t xr[2][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) ldmatrix4_trans(xr[k], xt + tile_off(16 * k + mtok, mpiece + 2 * half));
+    for (int half = 0; half < 2; ++half) ldmatrix4_trans(xr[half], xt + xq_off(mtok, mpiece + 2 * half));  // 16 value rows
+    uint64_t ws[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // 8 tokens: this lane's pair of them
-            const uint64_t ws = *reinterpret_cast<const uint64_t *>(w + 8 * j + 2 * (lane & 3));
+    for (int j = 0; j < 2; ++j) ws[j] = *reinterpret_cast<const uint64_t *>(w + 8 * j + 2 * (lane & 3));  // this lane's pair of 8 tokens
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t part[TERMS][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {  // value rows lane / 4 and + 8
-                const uint32_t x = xr[j >> 1][2 * (j & 1) + q];
-                uint64_t f = mul2(pair_bf(x), ws);
+                uint64_t f = mul2(pair_bf(xr[half][2 * j + q]), ws[j]);
 #pragma unroll
                 for (int i = 0; i < TERMS; ++i) {
                     const uint32_t word = pack_bf2(f);
@@ -226,9 +228,8 @@ __device__ __forceinline__ void convert_w(uint32_t trow, uint32_t xt, const floa
                     }
                 }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < TERMS; ++i) tmem_st_16x16(trow + ((uint32_t)(16 * half) << 16) + w_col(place, i), part[i]);
+        for (int i = 0; i < TERMS; ++i) tmem_st_16x8(at + ((uint32_t)(16 * half) << 16) + 8 * i, part[i]);
     }
 }
 
@@ -335,6 +336,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
               const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_y,
               const __grid_constant__ CUtensorMap map_z, const __grid_constant__ Args a) {
     using LY = Layout<DK, NH, GATE>;
+    constexpr int X_FREE = X_FULL + LY::NXQ, BARS = X_FREE + LY::NXQ;
     static_assert(LY::N_BAR == BARS, "barriers");
     // parts of the addends: 24 bits under an fp32 state, 16 under a bfloat16 one
     constexpr int TERMS = sizeof(ST) == 4 ? 3 : 2;
@@ -368,9 +370,10 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     if (tid == 0) {
         auto init = [&](int b, int count) { tc::mbar_init(&bars[b], count); };
         for (int b = 0; b < BARS; ++b) init(b, 1);
-        for (int b : {(int)S_READY, (int)W_FULL, (int)W_FULL + 1, (int)YS_READY}) init(b, 4);
+        for (int b : {(int)S_READY, (int)YS_READY}) init(b, 4);
+        for (int k = 0; k < W_PLACES; ++k) init(W_FULL + k, 4);
         for (int b : {(int)P_READY, (int)Y_FREE}) init(b, 8);
-        for (int k = 0; k < LY::NX; ++k) init(X_FREE + k, 8);
+        for (int k = 0; k < LY::NXQ; ++k) init(X_FREE + k, 2);
         for (int k = 0; k < 2; ++k) {
             init(SC_FULL + k, NH);
             init(SC_FREE + k, 20);
@@ -473,7 +476,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             arrive(P_READY);
             if (c > 0) {  // the previous chunk's stores have read x's place: it may be loaded again
                 if (lane == 0) tc::bulk_wait_read<0>();
-                arrive(X_FREE + (c - 1) % LY::NX);
+                arrive(X_FREE + (4 * (c - 1) + quad) % LY::NXQ);
             }
 
             // y of row t: Y + D x, gated; through x's place in shared memory to
@@ -484,15 +487,15 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             if (!wait_warp(&bars[Y_DONE], par, abort)) break;
             tc::tc_fence_after();
             tc::tmem_ld16(trow + T_Y + 64 * half, r0);
-            const uint4 *nf = reinterpret_cast<const uint4 *>(sm + LY::NF) + 4 * (c % LY::NX);
+            const uint4 *nf = reinterpret_cast<const uint4 *>(sm + LY::NF) + 4 * (c % LY::NF_CHUNKS);
             uint32_t any = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) any |= nf[j].x | nf[j].y | nf[j].z | nf[j].w;
             const bool direct = any || 32 * quad + 32 > m;
-            uint8_t *xp = sm + LY::x(c % LY::NX) + half * PANEL;
+            uint8_t *xp = sm + LY::x((4 * c + quad) % LY::NXQ) + half * (XQ / 2);  // the warp's 32 rows of x
             const uint32_t swz = (t & 7) << 4;
             auto x_at = [&](int k, int j) {  // 8 of 16 value columns
-                return reinterpret_cast<uint4 *>(xp + t * 128 + ((32 * k + 16 * j) ^ swz));
+                return reinterpret_cast<uint4 *>(xp + lane * 128 + ((32 * k + 16 * j) ^ swz));
             };
             auto columns = [&](auto direct_c) {
                 auto finish = [&](int k, const uint32_t (&y)[16], uint4 x0, uint4 x1) {
@@ -544,7 +547,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0 && live) {
-                    tc::tma_store_2d(&map_y, rw.col0 + 64 * half, row0 + c * Q + 32 * quad, xp + quad * 4096);
+                    tc::tma_store_2d(&map_y, rw.col0 + 64 * half, row0 + c * Q + 32 * quad, xp);
                     tc::bulk_commit();
                 }
             } else if (any && t < m && live) {
@@ -654,45 +657,44 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             tc::tc_fence_before();
         }
     } else if (warp < 16) {
-        // ------------------------------------------------ W from X (a warp's 32 value rows), every other 32 tokens
-        const int quad = warp & 3, place = (warp - 8) >> 2, r = 32 * quad + lane, h = NH == 2 ? r >> 6 : 0;
+        // ------------------------------------------------ W from X (a warp's 32 value rows), every other 16 tokens
+        const int quad = warp & 3, set = (warp - 8) >> 2, r = 32 * quad + lane, h = NH == 2 ? r >> 6 : 0;
         const uint32_t trow = tb + ((uint32_t)(32 * quad) << 16);
-        uint32_t *nf = reinterpret_cast<uint32_t *>(sm + LY::NF) + 4 * quad;
-        for (int c = 0; c < chunks; ++c) {
+        uint16_t *nf = reinterpret_cast<uint16_t *>(sm + LY::NF) + 8 * quad;
+        bool ok = true;
+        for (int c = 0; ok && c < chunks; ++c) {
             const uint32_t par = c & 1, par2 = (c >> 1) & 1;
             const int m = min(Q, len - c * Q);
-            const int xi = c % LY::NX;
-            uint8_t *xt = sm + LY::x(xi);
-            if (!wait_warp(&bars[X_FULL + xi], (uint32_t)(c / LY::NX) & 1, abort)) break;
             if (!wait_warp(&bars[SC_FULL + par], par2, abort)) break;
-            if (m < Q && !wait_warp(&bars[B_FULL], par, abort)) break;
+            if (m < Q && !wait_warp(&bars[B_FULL + par], par2, abort)) break;
             const float *w = scal(c, h) + Scal::W;
-            bool ok = true;
 #pragma unroll 1
-            for (int q = place; q < 4; q += 2) {  // 32 tokens
-                const int nq = 4 * c + q;
-                if (32 * q + 32 > m) {  // (the last chunk) zeros behind the segment, in X and B
+            for (int q = 0; q < 4; ++q) {  // 32 tokens, this set's 16 of them
+                const int nx = 4 * c + q, nw = 2 * nx + set, place = nw % W_PLACES, first = 32 * q + 16 * set;
+                uint8_t *xt = sm + LY::x(nx % LY::NXQ);
+                if (!(ok = wait_warp(&bars[X_FULL + nx % LY::NXQ], (uint32_t)(nx / LY::NXQ) & 1, abort))) break;
+                if (first + 16 > m) {  // (the last chunk) zeros behind the segment, in X and B
                     constexpr int BP = DK / 32;  // pieces of a row of b for each warp
-                    for (int k = lane; k < 32 * (4 + BP); k += 32) {
-                        const int row = 32 * q + k / (4 + BP), pc = k % (4 + BP);
-                        uint8_t *dst = pc < 4 ? xt + tile_off(row, 4 * quad + pc) : sm + LY::B + tile_off(row, BP * quad + pc - 4);
+                    for (int k = lane; k < 16 * (4 + BP); k += 32) {
+                        const int row = first + k / (4 + BP), pc = k % (4 + BP);
+                        uint8_t *dst = pc < 4 ? xt + xq_off(row & 31, 4 * quad + pc) : sm + LY::b(par) + tile_off(row, BP * quad + pc - 4);
                         if (row >= m) *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     tc::fence_async_smem();
                     __syncwarp();
                 }
-                if (nq >= 2) {  // the update that used this place has read it
-                    if (!(ok = wait_warp(&bars[W_FREE + place], (uint32_t)((nq >> 1) - 1) & 1, abort))) break;
+                if (nw >= W_PLACES) {  // the update that used this place has read it
+                    if (!(ok = wait_warp(&bars[W_FREE + place], (uint32_t)(nw / W_PLACES - 1) & 1, abort))) break;
                     tc::tc_fence_after();
                 }
                 uint32_t acc = 0u, mask = 0u;
-                const uint32_t xq = tc::smem_u32(xt) + 32 * 128 * q;
-                convert_w<TERMS, false>(trow, xq, w + 32 * q, place, quad, lane, acc);
+                const uint32_t at = trow + T_W + W_PLACE * place, x16 = tc::smem_u32(xt) + 16 * 128 * set;
+                convert_w<TERMS, false>(at, x16, w + first, quad, lane, acc);
                 if (__any_sync(0xffffffffu, saw_no_number(acc))) {
                     // again, without later parts that are no numbers; then x's own zeroed
-                    convert_w<TERMS, true>(trow, xq, w + 32 * q, place, quad, lane, acc);
-                    for (int s = 0; s < 32; ++s) {
-                        bf16 *xp = reinterpret_cast<bf16 *>(xt + tile_off(32 * q + s, r >> 3) + (r & 7) * 2);
+                    convert_w<TERMS, true>(at, x16, w + first, quad, lane, acc);
+                    for (int s = 0; s < 16; ++s) {
+                        bf16 *xp = reinterpret_cast<bf16 *>(xt + xq_off(16 * set + s, r >> 3) + (r & 7) * 2);
                         if (!(fabsf(to_f(*xp)) <= 3.4e38f)) {
                             *xp = __float2bfloat16_rn(0.f);
                             mask |= 1u << s;
@@ -701,13 +703,12 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     mask = __reduce_or_sync(0xffffffffu, mask);
                     tc::fence_async_smem();
                 }
-                if (lane == 0) nf[16 * xi + q] = mask;
-                if (q >= 2) arrive(SC_FREE + par);
+                if (lane == 0) nf[32 * (c % LY::NF_CHUNKS) + 2 * q + set] = (uint16_t)mask;
+                if (q == 3) arrive(SC_FREE + par);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 arrive(W_FULL + place);
             }
-            if (!ok) break;
         }
     } else if (warp == 20) {
         // ------------------------------------------------ loads
@@ -715,43 +716,54 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             tc::tma_prefetch_desc(&map_x);
             tc::tma_prefetch_desc(&map_b);
             tc::tma_prefetch_desc(&map_c);
-            auto load = [&](const CUtensorMap *map, int off, int panels, int col, int row, uint64_t *full) {
-                tc::mbar_arrive_expect_tx(full, panels * PANEL);
-                for (int k = 0; k < panels; ++k) tc::tma_load_2d(sm + off + k * PANEL, map, col + 64 * k, row, full);
+            auto load = [&](const CUtensorMap *map, int off, int panels, int bytes, int col, int row, uint64_t *full) {
+                tc::mbar_arrive_expect_tx(full, panels * bytes);
+                for (int k = 0; k < panels; ++k) tc::tma_load_2d(sm + off + k * bytes, map, col + 64 * k, row, full);
             };
+            // whatever has a free place, b first; given up on as the waits are
             int nb = 0, nx = 0, nc = 0;  // copies issued
-            auto load_b = [&]() { load(&map_b, LY::B, LY::KP, rw.g * DK, row0 + nb++ * Q, &bars[B_FULL]); };
-            auto load_c = [&]() { load(&map_c, LY::C, LY::KP, rw.g * DK, row0 + nc++ * Q, &bars[C_FULL]); };
-            auto load_x = [&]() {
-                load(&map_x, LY::x(nx % LY::NX), R / 64, rw.col0, row0 + nx * Q, &bars[X_FULL + nx % LY::NX]);
-                ++nx;
-            };
-            load_b();
-            load_x();
-            load_c();
-            if (chunks > 1) load_x();
-            for (int c = 0; c + 1 < chunks; ++c) {  // in the order in which the places become free
-                if (c + 2 < chunks) {
-                    if (c > 0 && !wait1(&bars[X_FREE + (c - 1) % LY::NX], (uint32_t)((c - 1) / LY::NX) & 1, abort)) break;
-                    load_x();
+            uint64_t t0 = globaltimer();
+            while (nb < chunks || nc < chunks || nx < 4 * chunks) {
+                const int before = nb + nc + nx;
+                if (nb < chunks && (nb < 2 || tc::mbar_try_wait(&bars[B_FREE + (nb & 1)], (uint32_t)((nb >> 1) - 1) & 1))) {
+                    load(&map_b, LY::b(nb & 1), LY::KP, PANEL, rw.g * DK, row0 + nb * Q, &bars[B_FULL + (nb & 1)]);
+                    ++nb;
                 }
-                if (!wait1(&bars[C_FREE], c & 1, abort)) break;
-                load_c();
-                if (!wait1(&bars[B_FREE], c & 1, abort)) break;
-                load_b();
+                if (nc < chunks && (nc < 1 || tc::mbar_try_wait(&bars[C_FREE], (uint32_t)(nc - 1) & 1))) {
+                    load(&map_c, LY::C, LY::KP, PANEL, rw.g * DK, row0 + nc * Q, &bars[C_FULL]);
+                    ++nc;
+                }
+                const int xp = nx % LY::NXQ;
+                if (nx < 4 * chunks && (nx < LY::NXQ || tc::mbar_try_wait(&bars[X_FREE + xp], (uint32_t)(nx / LY::NXQ - 1) & 1))) {
+                    load(&map_x, LY::x(xp), R / 64, XQ / 2, rw.col0, row0 + nx * 32, &bars[X_FULL + xp]);
+                    ++nx;
+                }
+                const uint64_t now = globaltimer();
+                if (nb + nc + nx > before) {
+                    t0 = now;
+                } else if (*abort || now - t0 > 2000000000ull) {
+                    if (!*abort) atomicOr(&g_ssm_faults, 1u);
+                    *abort = 1;
+                    break;
+                } else {
+                    __nanosleep(40);
+                }
             }
             // every copy has landed before the block may leave
-            drain(&bars[B_FULL], (nb - 1) & 1);
-            drain(&bars[C_FULL], (nc - 1) & 1);
-            for (int k = 0; k < LY::NX; ++k) {
-                const int x = (nx + LY::NX - 1 - k) / LY::NX;  // copies into place k
+            if (nb) drain(&bars[B_FULL + ((nb - 1) & 1)], (uint32_t)((nb - 1) >> 1) & 1);
+            if (nb > 1) drain(&bars[B_FULL + (nb & 1)], (uint32_t)((nb - 2) >> 1) & 1);
+            if (nc) drain(&bars[C_FULL], (uint32_t)(nc - 1) & 1);
+            for (int k = 0; k < LY::NXQ; ++k) {
+                const int x = (nx + LY::NXQ - 1 - k) / LY::NXQ;  // copies into place k
                 if (x) drain(&bars[X_FULL + k], (x - 1) & 1);
             }
         }
         __syncwarp();
     } else if (warp == 21) {
         // ------------------------------------------------ products
-        if (tc::elect_one()) {
+        {
+            const uint32_t lead = tc::elect_one() ? 1u : 0u;
+            const int n_chunks = __shfl_sync(0xffffffffu, chunks, 0);
             constexpr uint32_t ID_G = tc::instr_desc(tc::FMT_BF16, false, false, Q, Q);
             constexpr uint32_t ID_Y2 = tc::instr_desc(tc::FMT_BF16, false, false, Q, R);
             constexpr uint32_t ID_Y1 = tc::instr_desc(tc::FMT_BF16, false, true, Q, R / NH);
@@ -761,62 +773,65 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             // rows (K along the rows: its columns are the product's columns); those
             // of the others differ by a constant (in 16-byte units)
             auto kmajor = [&](int off) { return tc::smem_desc(tc::smem_u32(sm + off), 16, 1024, tc::SWZ_128); };
-            auto nmajor = [&](int off) { return tc::smem_desc(tc::smem_u32(sm + off), PANEL, 1024, tc::SWZ_128); };
+            auto nmajor = [&](int off, int panel) { return tc::smem_desc(tc::smem_u32(sm + off), panel, 1024, tc::SWZ_128); };
             constexpr uint64_t COLS = 32 / 16, PANELS = PANEL / 16, ROWS = 16 * 128 / 16;
             const uint64_t ck = kmajor(LY::C), sk = kmajor(LY::S);
-            const uint64_t bk = kmajor(LY::B), bn = nmajor(LY::B), xn = nmajor(LY::X);
+            const uint64_t bk = kmajor(LY::B), bn = nmajor(LY::B, PANEL), xn = nmajor(LY::X, XQ / 2);
+            constexpr uint64_t NEXT_B = LY::CTILE / 16, NEXT_X = XQ / 16;
             bool ok = true;
-            for (int c = 0; c < chunks; ++c) {
-                const uint32_t par = c & 1;
+            for (int c = 0; c < n_chunks; ++c) {
+                const uint32_t par = c & 1, par2 = (c >> 1) & 1;
                 // A B^T over DK columns of two tiles
                 auto over_columns = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t id) {
 #pragma unroll
                     for (int pn = 0; pn < LY::KP; ++pn)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            tc::mma_ss_f16(d, ad + pn * PANELS + k * COLS, bd + pn * PANELS + k * COLS, id, pn + k > 0);
+                            tc::mma_ss_f16_by(lead, d, ad + pn * PANELS + k * COLS, bd + pn * PANELS + k * COLS, id, pn + k > 0);
                 };
-                // S' of 64 tokens
-                auto update = [&](int half) {
-                    const uint64_t bd = bn + half * 4 * ROWS;
-#pragma unroll
-                    for (int place = 0; place < 2; ++place) {
-                        if (!wait1(&bars[W_FULL + place], (uint32_t)half, abort)) return false;  // (two uses a chunk)
+                // S' of 16 tokens g ..
+                auto update = [&](int from, int to) {
+#pragma unroll 1
+                    for (int g = from; g < to; ++g) {
+                        const int nw = 8 * c + g, place = nw % W_PLACES;
+                        if (!wait_warp(&bars[W_FULL + place], (uint32_t)(nw / W_PLACES) & 1, abort)) return false;
                         tc::tc_fence_after();
 #pragma unroll
                         for (int i = 0; i < TERMS; ++i)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                tc::mma_ts_f16(tb + T_S, tb + w_col(place, i) + 8 * k, bd + (2 * place + k) * ROWS, ID_S, true);
-                        tc::mma_commit(&bars[W_FREE + place]);
+                            tc::mma_ts_f16_by(lead, tb + T_S, tb + T_W + W_PLACE * place + 8 * i, bn + par * NEXT_B + g * ROWS, ID_S, true);
+                        tc::mma_commit_by(lead, &bars[W_FREE + place]);
                     }
                     return true;
                 };
-                if (!(ok = wait1(&bars[C_FULL], par, abort) && wait1(&bars[B_FULL], par, abort))) break;
+                if (!(ok = wait_warp(&bars[C_FULL], par, abort) && wait_warp(&bars[B_FULL + par], par2, abort))) break;
                 tc::tc_fence_after();
-                over_columns(tb + T_G, ck, bk, ID_G);
-                tc::mma_commit(&bars[G_DONE]);
-                if (!(ok = wait1(&bars[S_READY], par, abort) && update(0))) break;
-                if (!(ok = c == 0 || wait1(&bars[Y_FREE], (c - 1) & 1, abort))) break;
+                over_columns(tb + T_G, ck, bk + par * NEXT_B, ID_G);
+                tc::mma_commit_by(lead, &bars[G_DONE]);
+                if (!(ok = wait_warp(&bars[S_READY], par, abort) && update(0, W_PLACES))) break;
+                if (!(ok = c == 0 || wait_warp(&bars[Y_FREE], (c - 1) & 1, abort))) break;
                 tc::tc_fence_after();
                 over_columns(tb + T_Y, ck, sk, ID_Y2);
-                tc::mma_commit(&bars[Y2_DONE]);
-                tc::mma_commit(&bars[C_FREE]);
-                if (!(ok = update(1))) break;
-                tc::mma_commit(&bars[ST_DONE]);
-                tc::mma_commit(&bars[B_FREE]);
-                if (!(ok = wait1(&bars[P_READY], par, abort) && wait1(&bars[YS_READY], par, abort))) break;
+                tc::mma_commit_by(lead, &bars[Y2_DONE]);
+                tc::mma_commit_by(lead, &bars[C_FREE]);
+                if (!(ok = update(W_PLACES, 8))) break;
+                tc::mma_commit_by(lead, &bars[ST_DONE]);
+                tc::mma_commit_by(lead, &bars[B_FREE + par]);
+                if (!(ok = wait_warp(&bars[P_READY], par, abort) && wait_warp(&bars[YS_READY], par, abort))) break;
                 tc::tc_fence_after();
-                const uint64_t xd = xn + (c % LY::NX) * (LY::XTILE / 16);
 #pragma unroll
-                for (int h = 0; h < NH; ++h)
+                for (int q = 0; q < 4; ++q) {  // (32 tokens of x)
+                    const uint64_t xd = xn + (uint64_t)((4 * c + q) % LY::NXQ) * NEXT_X;
 #pragma unroll
-                    for (int k = 0; k < Q / 16; ++k)
-                        tc::mma_ts_f16(tb + T_Y + (R / NH) * h, tb + p_col(k, h), xd + h * PANELS + k * ROWS, ID_Y1, true);
-                tc::mma_commit(&bars[Y_DONE]);
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            tc::mma_ts_f16_by(lead, tb + T_Y + (R / NH) * h, tb + p_col(2 * q + k, h), xd + h * (XQ / 32) + k * ROWS, ID_Y1,
+                                           true);
+                }
+                tc::mma_commit_by(lead, &bars[Y_DONE]);
             }
             if (!ok) {  // products in flight have completed before tensor memory is freed
-                tc::mma_commit(&bars[DRAIN]);
+                tc::mma_commit_by(lead, &bars[DRAIN]);
                 drain(&bars[DRAIN], 0);
             }
         }
@@ -858,7 +873,8 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     using LY = EndLayout<DK, NH>;
     constexpr int TERMS = 3;
     enum { B_FULL, FREE = B_FULL + 2, X_FULL = FREE + 2, SC_FULL = X_FULL + 2, SC_FREE = SC_FULL + 2, W_FULL = SC_FREE + 2,
-           W_FREE = W_FULL + 4, DONE = W_FREE + 4, BARS };  // (a place of W for each 32 tokens of a chunk)
+           W_FREE = W_FULL + 8, DONE = W_FREE + 8, BARS };  // (a place of W for each 16 tokens of a chunk)
+    constexpr int T_W8 = 256;
     static_assert(LY::N_BAR == BARS, "barriers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -912,20 +928,19 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             if (!(ok = wait_warp(&bars[X_FULL + par], par2, abort) && wait_warp(&bars[SC_FULL + par], par2, abort))) break;
             const float *w = weights(c, h);
 #pragma unroll 1
-            for (int q = set; q < 4; q += 2) {
+            for (int g = set; g < 8; g += 2) {  // 16 tokens
                 if (c > 0) {
-                    if (!(ok = wait_warp(&bars[W_FREE + q], (uint32_t)(c - 1) & 1, abort))) break;
+                    if (!(ok = wait_warp(&bars[W_FREE + g], (uint32_t)(c - 1) & 1, abort))) break;
                     tc::tc_fence_after();
                 }
                 uint32_t acc = 0u;
-                const uint32_t xq = tc::smem_u32(sm + LY::x(par)) + 32 * 128 * q;
-                convert_w<TERMS, false>(trow, xq, w + 32 * q, q - 2, quad, lane, acc);
-                if (__any_sync(0xffffffffu, saw_no_number(acc)))
-                    convert_w<TERMS, true>(trow, xq, w + 32 * q, q - 2, quad, lane, acc);
-                if (q >= 2) arrive(SC_FREE + par);
+                const uint32_t at = trow + T_W8 + W_PLACE * g, x16 = tc::smem_u32(sm + LY::x(par, g >> 1)) + 16 * 128 * (g & 1);
+                convert_w<TERMS, false>(at, x16, w + 16 * g, quad, lane, acc);
+                if (__any_sync(0xffffffffu, saw_no_number(acc))) convert_w<TERMS, true>(at, x16, w + 16 * g, quad, lane, acc);
+                if (g >= 6) arrive(SC_FREE + par);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
-                arrive(W_FULL + q);
+                arrive(W_FULL + g);
             }
         }
         if (ok && set == 0 && wait_warp(&bars[DONE], 0, abort) && (h == 0 || rw.two)) {
@@ -950,9 +965,10 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             for (int c = 0; c < chunks; ++c) {
                 const int k = c & 1, row = row0 + (chunks - 1 - c) * Q;
                 if (c >= 2 && !wait1(&bars[FREE + k], (uint32_t)((c >> 1) - 1) & 1, abort)) break;
-                tc::mbar_arrive_expect_tx(&bars[X_FULL + k], LY::XTILE);
-                for (int j = 0; j < R / 64; ++j)
-                    tc::tma_load_2d(sm + LY::x(k) + j * PANEL, &map_x, rw.col0 + 64 * j, row, &bars[X_FULL + k]);
+                tc::mbar_arrive_expect_tx(&bars[X_FULL + k], 4 * XQ);
+                for (int q = 0; q < 4; ++q)
+                    for (int j = 0; j < R / 64; ++j)
+                        tc::tma_load_2d(sm + LY::x(k, q) + j * (XQ / 2), &map_x, rw.col0 + 64 * j, row + 32 * q, &bars[X_FULL + k]);
                 tc::mbar_arrive_expect_tx(&bars[B_FULL + k], LY::CTILE);
                 for (int j = 0; j < LY::KP; ++j)
                     tc::tma_load_2d(sm + LY::b(k) + j * PANEL, &map_b, rw.g * DK + 64 * j, row, &bars[B_FULL + k]);
@@ -969,29 +985,28 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         __syncwarp();
     } else if (warp == 9) {
         // ------------------------------------------------ products
-        if (tc::elect_one()) {
+        {
+            const uint32_t lead = tc::elect_one() ? 1u : 0u;
+            const int n_chunks = __shfl_sync(0xffffffffu, chunks, 0);
             constexpr uint32_t ID_S = tc::instr_desc(tc::FMT_BF16, false, true, R, DK);
             constexpr uint64_t ROWS = 16 * 128 / 16;
             bool ok = true;
-            for (int c = 0; ok && c < chunks; ++c) {
+            for (int c = 0; ok && c < n_chunks; ++c) {
                 const uint32_t par = c & 1;
                 const uint64_t bd = tc::smem_desc(tc::smem_u32(sm + LY::b(par)), PANEL, 1024, tc::SWZ_128);
-                if (!(ok = wait1(&bars[B_FULL + par], (c >> 1) & 1, abort))) break;
+                if (!(ok = wait_warp(&bars[B_FULL + par], (c >> 1) & 1, abort))) break;
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    if (!(ok = wait1(&bars[W_FULL + q], par, abort))) break;
+                for (int g = 0; g < 8; ++g) {
+                    if (!(ok = wait_warp(&bars[W_FULL + g], par, abort))) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < TERMS; ++i)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            tc::mma_ts_f16(tb + T_S, tb + w_col(q - 2, i) + 8 * k, bd + (2 * q + k) * ROWS, ID_S,
-                                           c + q + i + k > 0);
-                    tc::mma_commit(&bars[W_FREE + q]);
+                        tc::mma_ts_f16_by(lead, tb + T_S, tb + T_W8 + W_PLACE * g + 8 * i, bd + g * ROWS, ID_S, c + g + i > 0);
+                    tc::mma_commit_by(lead, &bars[W_FREE + g]);
                 }
-                if (ok) tc::mma_commit(&bars[FREE + par]);  // (W of the chunk has been made, so x has been read too)
+                if (ok) tc::mma_commit_by(lead, &bars[FREE + par]);  // (W of the chunk has been made, so x has been read too)
             }
-            tc::mma_commit(&bars[DONE]);
+            tc::mma_commit_by(lead, &bars[DONE]);
             if (!ok) drain(&bars[DONE], 0);
         }
         __syncwarp();
@@ -1086,7 +1101,7 @@ cudaError_t launch_typed(const SsmParams &p, const SeqIdx &q, void *work, cudaSt
     if (e != cudaSuccess) return e;
     CUtensorMap mx, mb, mc, my, mz;
     const dl_ssm &in = p.in;
-    if ((e = row_map(&mx, in.x, (long long)p.H * p.dv, q.T, in.x_stride)) != cudaSuccess) return e;
+    if ((e = row_map(&mx, in.x, (long long)p.H * p.dv, q.T, in.x_stride, 32)) != cudaSuccess) return e;
     if ((e = row_map(&mb, in.b, (long long)p.G * DK, q.T, in.b_stride)) != cudaSuccess) return e;
     if ((e = row_map(&mc, in.c, (long long)p.G * DK, q.T, in.c_stride)) != cudaSuccess) return e;
     const long long yw = (long long)p.H * p.dv;

@@ -26,6 +26,12 @@ DL_HD inline constexpr int tile_off(int row, int piece) {
     return (piece >> 3) * PANEL + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
+// x is held by quarters of a chunk: 32 tokens, two panels of 64 columns.
+constexpr int XQ = 2 * 32 * 128;
+DL_HD inline constexpr int xq_off(int row, int piece) {
+    return (piece >> 3) * (XQ / 2) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+
 // Byte of (row, 16-byte piece) of a warp's gate block: 32 rows of 16 columns under 32-byte swizzle.
 DL_HD inline constexpr int gate_off(int row, int piece) { return row * 32 + ((piece ^ ((row >> 2) & 1)) << 4); }
 
@@ -40,20 +46,22 @@ struct Scal {
 template <int DK, int NH, bool GATE>
 struct Layout {
     static constexpr int KP = DK / 64;          // panels of b, c and the state
-    static constexpr int CTILE = KP * PANEL, XTILE = (R / 64) * PANEL, STILE = KP * PANEL;
-    static constexpr int NX = 3;  // chunks of x in flight
-    static constexpr int C = 0, B = C + CTILE, X = B + CTILE, S = X + NX * XTILE, Z = S + STILE;
+    static constexpr int CTILE = KP * PANEL, STILE = KP * PANEL;
+    static constexpr int NXQ = GATE ? 8 : 11;  // quarters of x held: what fits at DK = 128
+    static constexpr int C = 0, B = C + CTILE, S = B + 2 * CTILE, X = S + STILE, Z = X + NXQ * XQ;
+    static constexpr int NF_CHUNKS = 3;
     static constexpr int NZ = 3, ZBLOCK = 32 * 32;  // gate blocks in flight for each of 8 warps
     static constexpr int SCAL = Z + (GATE ? 8 * NZ * ZBLOCK : 0);
     static constexpr int SCAL_BYTES = Scal::FLOATS * 4;                 // one head of one chunk
-    static constexpr int NF = SCAL + 2 * NH * SCAL_BYTES;               // masks of rows with no number: [NX][4 warps][4]
-    static constexpr int BAR = NF + NX * 16 * 4;
-    static constexpr int N_BAR = 51;
+    static constexpr int NF = SCAL + 2 * NH * SCAL_BYTES;               // masks of tokens with no number: [chunks][4 warps][Q bits]
+    static constexpr int BAR = NF + NF_CHUNKS * 16 * 4;
+    static constexpr int N_BAR = 53 + 2 * NXQ;
     static constexpr int TSLOT = BAR + 8 * N_BAR, ABORT = TSLOT + 4, BYTES = ABORT + 12;
     static constexpr int REQUEST = BYTES + 1024;  // the kernel aligns its base to 1024
     static_assert(REQUEST <= SMEM_LIMIT, "shared memory of a block");
     static_assert(SCAL_BYTES % 16 == 0 && NF % 16 == 0 && BAR % 8 == 0, "alignment");
-    DL_HD static constexpr int x(int i) { return X + i * XTILE; }
+    DL_HD static constexpr int b(int i) { return B + i * CTILE; }
+    DL_HD static constexpr int x(int i) { return X + i * XQ; }
     DL_HD static constexpr int z(int warp, int i) { return Z + (warp * NZ + i) * ZBLOCK; }
     DL_HD static constexpr int scal(int i, int h) { return SCAL + (i * NH + h) * SCAL_BYTES; }
 };
@@ -61,25 +69,24 @@ struct Layout {
 // The kernel of segments' end states: b and x in two buffers, a chunk's weights.
 template <int DK, int NH>
 struct EndLayout {
-    static constexpr int KP = DK / 64, CTILE = KP * PANEL, XTILE = (R / 64) * PANEL;
-    static constexpr int B = 0, X = 2 * CTILE, SCAL = X + 2 * XTILE, SCAL_BYTES = Q * 4;
-    static constexpr int BAR = SCAL + 2 * NH * SCAL_BYTES, N_BAR = 19;
+    static constexpr int KP = DK / 64, CTILE = KP * PANEL;
+    static constexpr int B = 0, X = 2 * CTILE, SCAL = X + 2 * 4 * XQ, SCAL_BYTES = Q * 4;
+    static constexpr int BAR = SCAL + 2 * NH * SCAL_BYTES, N_BAR = 27;
     static constexpr int TSLOT = BAR + 8 * N_BAR, ABORT = TSLOT + 4, BYTES = ABORT + 12;
     static constexpr int REQUEST = BYTES + 1024;
     static_assert(REQUEST <= SMEM_LIMIT, "shared memory of a block");
     DL_HD static constexpr int b(int i) { return B + i * CTILE; }
-    DL_HD static constexpr int x(int i) { return X + i * XTILE; }
+    DL_HD static constexpr int x(int i, int q) { return X + (4 * i + q) * XQ; }
     DL_HD static constexpr int scal(int i, int h) { return SCAL + (i * NH + h) * SCAL_BYTES; }
 };
 
 // Tensor-memory columns (fp32 words): the state [R x DK]; the scores C B^T
 // [Q x Q], overwritten 16 columns at a time by the decayed scores as bf16
 // pairs (8 columns of each of one or two heads); the outputs [Q x R]; the
-// decayed addends of 32 tokens [R x 32] as bf16 pairs in up to three parts of
-// 16 columns, in two places used in turn (the kernel of end states, which has
-// neither scores nor outputs, uses two more in front of them: -2 and -1).
-constexpr int T_S = 0, T_G = 128, T_Y = 256, T_W = 384, T_COLS = 512;
-DL_HD inline constexpr int w_col(int place, int part) { return T_W + 64 * place + 16 * part; }
+// decayed addends of 16 tokens [R x 16] as bf16 pairs in up to three parts of 8
+// columns, in five places used in turn (the kernel of end states, which has
+// neither scores nor outputs, has eight from column 256 on).
+constexpr int T_S = 0, T_G = 128, T_Y = 256, T_W = 384, T_COLS = 512, W_PLACE = 24, W_PLACES = 5;
 // Columns of head h's decayed scores of tokens 16 k .. 16 k + 15.
 DL_HD inline constexpr int p_col(int k, int h) { return T_G + 16 * k + 8 * h; }
 
