@@ -72,8 +72,8 @@ DL_HD inline int segs_of(int n, int len) { return (int)(((long long)n + len - 1)
 // sequence's chunks in order, so few or uneven sequences leave the GPU idle;
 // split, each segment's end state comes first (about 0.4 of a chunk's time
 // each), then the segments run side by side. One sequence: as many segments as
-// fill the GPU. Several, whose lengths the host does not know: segments of 1.4
-// times an SM's even share, which only a sequence well above it exceeds. Both
+// fill the GPU. Several, whose lengths the host does not know: segments of twice
+// an SM's even share, which only a sequence well above it exceeds. Both
 // need at least 4 chunks a segment, and to beat the longest sequence there can
 // be, unsplit, by more than the two launches they cost (about 8 chunks).
 DL_HD inline int seg_len_for(int T, int n_seq, long long units, int chunk, int sms) {
@@ -85,7 +85,7 @@ DL_HD inline int seg_len_for(int T, int n_seq, long long units, int chunk, int s
         if (n < 2) return 0;
         len = (chunks + n - 1) / n;
     } else {
-        len = (7 * chunks * units + 5LL * sms - 1) / (5LL * sms);
+        len = (2 * chunks * units + sms - 1) / sms;
         if (len < 4) len = 4;
     }
     if (10 * chunks <= 14 * len + 80) return 0;

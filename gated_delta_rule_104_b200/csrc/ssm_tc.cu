@@ -423,13 +423,16 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             tc::tc_fence_after();
             uint32_t r0[16], r1[16];  // 16 columns each, one being loaded
             tc::tmem_ld16(trow + T_G + 16 * half, r0);
+            float lth[NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) lth[h] = scal(c, h)[Scal::L + t];
             // P of tokens 16 k .. 16 k + 15 from their scores
             auto decayed = [&](int k, const uint32_t (&g)[16], bool diagonal) {
                 uint32_t pw[8];
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     const float *sc = scal(c, h);
-                    const float lt = sc[Scal::L + t];
+                    const float lt = lth[h];
                     if (!diagonal) {
                         const float v = exp2_fast(lt - sc[Scal::RB + (k >> 1)]);
                         const uint64_t vv = pair(v, v);
