@@ -234,8 +234,6 @@ __device__ __forceinline__ void convert_w(uint32_t at, uint32_t xt, const float 
 }
 
 // 16 columns of a state row.
-__device__ __forceinline__ void load_row16(const float *p, float (&v)[16]) { load_vec<16>(p, v); }
-__device__ __forceinline__ void load_row16(const bf16 *p, float (&v)[16]) { load_vec<16>(p, v); }
 __device__ __forceinline__ void store_row16(float *p, const uint32_t (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4 *>(p + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -388,6 +386,31 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tb = __shfl_sync(0xffffffffu, *tslot, 0);
+    // the state in front of the segment, DK / 4 columns of a row a thread of the first 16 warps
+    if (warp < 16) {
+        const int r = 32 * (warp & 3) + lane, h = NH == 2 ? r >> 6 : 0, col = (warp >> 2) * (DK / 4);
+        const long long srow = (long long)(rw.h0 + h) * p.dv + rw.r0 + (NH == 2 ? r & 63 : r);
+        float f[DK / 4];
+#pragma unroll
+        for (int j = 0; j < DK / 4; ++j) f[j] = 0.f;
+        if (h == 0 || rw.two) {
+            if (segs > 1)
+                load_vec<DK / 4>(a.seg_state + ((long long)(seg_base(s0, a.seg_len) + seg) * p.H * p.dv + srow) * DK + col, f);
+            else
+                load_vec<DK / 4>(static_cast<const ST *>(p.S) + ((long long)slot * p.H * p.dv + srow) * DK + col, f);
+        }
+#pragma unroll
+        for (int k = 0; k < DK / 64; ++k) {
+            uint32_t v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(f[16 * k + j]);
+            tc::tmem_st16(tb + ((uint32_t)(32 * (warp & 3)) << 16) + T_S + col + 16 * k, v);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+    }
+    __syncthreads();
+    tc::tc_fence_after();
     auto scal = [&](int c, int h) { return reinterpret_cast<float *>(sm + LY::scal(c & 1, h)); };
     auto arrive = [&](int b) {  // once per warp, after every lane's writes
         __syncwarp();
@@ -591,33 +614,15 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 scale16(v, e);
                 tc::tmem_st16(trow + T_S + 16 * k, v);
             };
-            if (c == 0) {  // the state in front of the segment
+            tc::tmem_ld16(trow + T_S, r0);
 #pragma unroll 1
-                for (int k = 0; k < DK / 16; ++k) {
-                    float f[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = 0.f;
-                    if (live) {
-                        if (segs > 1)
-                            load_row16(a.seg_state + ((long long)(seg_base(s0, a.seg_len) + seg) * p.H * p.dv + srow) * DK + 16 * k, f);
-                        else
-                            load_row16(S + 16 * k, f);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) r0[j] = __float_as_uint(f[j]);
-                    advance(k, r0);
-                }
-            } else {
-                tc::tmem_ld16(trow + T_S, r0);
-#pragma unroll 1
-                for (int k = 0; k < DK / 16; k += 2) {
-                    tc::tmem_wait_ld();
-                    tc::tmem_ld16(trow + T_S + 16 * k + 16, r1);
-                    advance(k, r0);
-                    tc::tmem_wait_ld();
-                    if (k + 2 < DK / 16) tc::tmem_ld16(trow + T_S + 16 * k + 32, r0);
-                    advance(k + 1, r1);
-                }
+            for (int k = 0; k < DK / 16; k += 2) {
+                tc::tmem_wait_ld();
+                tc::tmem_ld16(trow + T_S + 16 * k + 16, r1);
+                advance(k, r0);
+                tc::tmem_wait_ld();
+                if (k + 2 < DK / 16) tc::tmem_ld16(trow + T_S + 16 * k + 32, r0);
+                advance(k + 1, r1);
             }
             tc::fence_async_smem();
             tc::tmem_wait_st();
