@@ -460,52 +460,94 @@ def dl_pool_flush(pool: Pool, slot, stream=None) -> None:
 
 # ------------------------------------------------------------------ norm, short convolution, selective scan
 
-def _rows(t, name: str, shape):
-    """Pointer and row stride of a CUDA tensor of the given shape whose rows (all
-    dimensions but the first) are contiguous."""
+# (These calls take a dozen tensors and a kernel of a few microseconds: what is
+# checked of a tensor is checked in one function, by the cheapest queries.)
+
+_codes = None
+
+
+def _code_of(t) -> int:
+    """dl_dtype of a tensor (as _dtype_code, 8-bit types too)."""
+    global _codes
+    if _codes is None:
+        torch = _torch()
+        _codes = {torch.float32: DL_F32, torch.bfloat16: DL_BF16, torch.int8: DL_I8, torch.float8_e4m3fn: DL_E4M3}
+    try:
+        return _codes[t.dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {t.dtype}") from None
+
+
+def _float_code(*ts) -> int:
+    """The one dl_dtype, float32 or bfloat16, of the tensors that are not None."""
+    code = _code_of(ts[0])
+    for t in ts:
+        if t is not None and t.dtype != ts[0].dtype:
+            raise TypeError("these operands must share one dtype: " + ", ".join(str(u.dtype) for u in ts if u is not None))
+    if code > DL_BF16:
+        raise TypeError(f"unsupported dtype {ts[0].dtype} (float32 or bfloat16)")
+    return code
+
+
+def _device() -> int:
+    """The current device: a call launches there, and every operand must lie on it."""
+    return _torch()._C._cuda_getDevice()
+
+
+def _misplaced(t, name: str, dev: int):
     if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != shape:
+        return ValueError(f"{name} must be a CUDA tensor")
+    return ValueError(f"{name} lies on {t.device}, but the current device is cuda:{dev}")
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+def _full(t, name: str, shape, dev: int) -> int:
+    """Pointer of a contiguous tensor of the given shape on the current device."""
+    if t.get_device() != dev:
+        raise _misplaced(t, name, dev)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    n = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != n:
-            raise ValueError(f"the rows of {name} must be contiguous")
-        n *= size
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(n, 1))
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _full(t, name: str, shape, dtype=None, optional: bool = False) -> Optional[int]:
-    """Pointer of a contiguous CUDA tensor of the given shape (and dtype)."""
-    if t is None and optional:
+def _f32(t, name: str, shape, dev: int) -> Optional[int]:
+    """The same of a float32 tensor, or None."""
+    if t is None:
         return None
-    p = _ptr(t, name)
-    if tuple(t.shape) != shape:
+    if _code_of(t) != DL_F32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    return _full(t, name, shape, dev)
+
+
+def _rows(t, name: str, shape, dev: int):
+    """Pointer and row stride of a tensor whose rows (all dimensions but the first) are contiguous."""
+    if t.get_device() != dev:
+        raise _misplaced(t, name, dev)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return p
+    width = 1
+    strides = t.stride()
+    for k in range(len(shape) - 1, 0, -1):
+        if shape[k] != 1 and strides[k] != width:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        width *= shape[k]
+    return t.data_ptr(), strides[0] if shape[0] > 1 else max(width, 1)
 
 
-def _same_device(first, *rest) -> None:
-    """Every tensor on the current device (the stream's): a call launches there."""
-    dev = _torch().cuda.current_device() if first.is_cuda else -1
-    for t in (first, *rest):
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("every operand must be a CUDA tensor")
-        if t.device.index != dev:
-            raise ValueError(f"a tensor lies on {t.device}, but the current device is cuda:{dev}")
-
-
-def _code8(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.int8:
-        return DL_I8
-    if t.dtype == torch.float8_e4m3fn:
-        return DL_E4M3
-    raise TypeError(f"unsupported dtype {t.dtype} (int8 or float8_e4m3fn)")
+def _index(t, name: str, n: int, dev: int) -> Optional[int]:
+    """Pointer of an int32 tensor of n elements, or None."""
+    if t is None:
+        return None
+    if t.dtype != _torch().int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    return _full(t, name, (n,), dev)
 
 
 def dl_rms_norm(x, weight, eps: float, y, residual=None, residual_out=None, scale=None, group: int = 0,
@@ -515,60 +557,58 @@ def dl_rms_norm(x, weight, eps: float, y, residual=None, residual_out=None, scal
     ``residual_out`` receives (it may be ``residual``). y is float32, bfloat16, or
     int8 / float8_e4m3fn codes with float32 ``scale`` [rows] (``group`` 0) or
     [rows, ceil(width / 128)] (``group`` 128)."""
-    torch = _torch()
     if x.dim() != 2:
         raise ValueError("x must be [rows, width]")
-    rows, width = x.shape
-    coded = y.dtype in (torch.int8, torch.float8_e4m3fn)
-    if coded and scale is None:
-        raise ValueError("an 8-bit y needs a scale")
-    if coded and scale.numel() != rows * (-(-width // group) if group else 1):
-        raise ValueError(f"scale has {scale.numel()} elements, expected rows x groups")
+    dev = _device() if x.is_cuda else -2
+    rows, width = shape = x.shape
+    xp, xs = _rows(x, "x", shape, dev)
+    xc, yc = _float_code(x), _code_of(y)
     if (residual is None) != (residual_out is None):
         raise ValueError("residual and residual_out go together")
-    if residual is not None and residual.dtype != residual_out.dtype:
-        raise TypeError("residual and residual_out must share one dtype")
-    if scale is not None and scale.dtype != torch.float32:
-        raise TypeError("scale must be float32")
-    _same_device(x, weight, y, residual, residual_out, scale)
-    xp, xs = _rows(x, "x", (rows, width))
-    args = (xp, _dtype_code(x), xs, _full(residual, "residual", (rows, width), optional=True),
-            _full(residual_out, "residual_out", (rows, width), optional=True),
-            DL_F32 if residual is None else _dtype_code(residual), _full(weight, "weight", (width,)), _dtype_code(weight),
-            float(eps), _full(y, "y", (rows, width)), _code8(y) if coded else _dtype_code(y),
-            _ptr(scale, "scale", True), int(group), rows, width, _stream(stream))
-    check("dl_rms_norm", load().dl_rms_norm(*args))
+    rp = rop = sp = None
+    rc = DL_F32
+    if residual is not None:
+        rc = _float_code(residual, residual_out)
+        rp, rop = _full(residual, "residual", shape, dev), _full(residual_out, "residual_out", shape, dev)
+    if scale is not None:
+        sp = _scales(scale, rows, width, group, dev)
+    elif yc > DL_BF16:
+        raise ValueError("an 8-bit y needs a scale")
+    status = load().dl_rms_norm(xp, xc, xs, rp, rop, rc, _full(weight, "weight", (width,), dev), _float_code(weight), eps,
+                                _full(y, "y", shape, dev), yc, sp, group, rows, width, _raw_stream(stream, dev))
+    if status:
+        check("dl_rms_norm", status)
+
+
+def _scales(scale, rows: int, width: int, group: int, dev: int) -> int:
+    n = rows * (-(-width // group) if group > 0 else 1)
+    if scale.numel() != n:
+        raise ValueError(f"scale has {scale.numel()} elements, expected {n} (rows x groups)")
+    return _f32(scale, "scale", scale.shape, dev)
 
 
 def dl_rows_from_8bit(codes, scale, out, group: int = 0, stream=None) -> None:
     """The values code * scale of dl_rms_norm's 8-bit rows into ``out`` (float32 or bfloat16)."""
     if codes.dim() != 2:
         raise ValueError("codes must be [rows, width]")
-    rows, width = codes.shape
-    if scale.numel() != rows * (-(-width // group) if group else 1):
-        raise ValueError(f"scale has {scale.numel()} elements, expected rows x groups")
-    if scale.dtype != _torch().float32:
-        raise TypeError("scale must be float32")
-    _same_device(codes, scale, out)
-    args = (_full(codes, "codes", (rows, width)), _code8(codes), _ptr(scale, "scale"), int(group),
-            _full(out, "out", (rows, width)), _dtype_code(out), rows, width, _stream(stream))
-    check("dl_rows_from_8bit", load().dl_rows_from_8bit(*args))
+    dev = _device() if codes.is_cuda else -2
+    rows, width = shape = codes.shape
+    status = load().dl_rows_from_8bit(_full(codes, "codes", shape, dev), _code_of(codes), _scales(scale, rows, width, group, dev),
+                                      group, _full(out, "out", shape, dev), _float_code(out), rows, width,
+                                      _raw_stream(stream, dev))
+    if status:
+        check("dl_rows_from_8bit", status)
 
 
-def _index(t, name: str, n: int, optional: bool) -> Optional[int]:
-    return _full(t, name, (n,), _torch().int32, optional)
-
-
-def _conv(x, w, bias, state, y, silu):
+def _conv(x, w, bias, state, y, silu, dev):
     if x.dim() != 2 or w.dim() != 2 or state.dim() != 3:
         raise ValueError("x must be [rows, channels], w [channels, taps], state [P, taps - 1, channels]")
     rows, channels = x.shape
     taps, P = w.shape[1], state.shape[0]
-    dt = _in_dtype(x, w, bias, state, y)
-    cv = dl_conv(_full(w, "w", (channels, taps)), _full(bias, "bias", (channels,), optional=True), channels, taps, dt,
-                 1 if silu else 0)
-    xp, xs = _rows(x, "x", (rows, channels))
-    return cv, xp, xs, rows, _full(state, "state", (P, taps - 1, channels)), P, _full(y, "y", (rows, channels))
+    xp, xs = _rows(x, "x", x.shape, dev)
+    cv = dl_conv(_full(w, "w", (channels, taps), dev), None if bias is None else _full(bias, "bias", (channels,), dev), channels,
+                 taps, _float_code(x, w, bias, state, y), 1 if silu else 0)
+    return cv, xp, xs, rows, _full(state, "state", (P, taps - 1, channels), dev), P, _full(y, "y", (rows, channels), dev)
 
 
 def dl_conv_prompt(x, w, bias, state, seq_start, slot, y, silu: bool = True, status=None, stream=None) -> None:
@@ -576,35 +616,41 @@ def dl_conv_prompt(x, w, bias, state, seq_start, slot, y, silu: bool = True, sta
     strided), w [channels, taps], bias [channels] or None, state [P, taps - 1,
     channels] (each slot's last inputs, read and replaced), seq_start [n + 1]
     int32, slot [n] int32 or None, y [T, channels]."""
-    cv, xp, xs, T, sp, P, yp = _conv(x, w, bias, state, y, silu)
+    dev = _device() if x.is_cuda else -2
+    cv, xp, xs, T, sp, P, yp = _conv(x, w, bias, state, y, silu, dev)
     n = seq_start.numel() - 1
-    _same_device(x, w, bias, state, seq_start, slot, y, status)
-    st = load().dl_conv_prompt(ctypes.byref(cv), xp, xs, T, _index(seq_start, "seq_start", n + 1, False), n, sp, P,
-                               _index(slot, "slot", n, True), _index(status, "status", 1, True), yp, _stream(stream))
-    check("dl_conv_prompt", st)
+    st = load().dl_conv_prompt(ctypes.byref(cv), xp, xs, T, _index(seq_start, "seq_start", n + 1, dev), n, sp, P,
+                               _index(slot, "slot", n, dev), _index(status, "status", 1, dev), yp, _raw_stream(stream, dev))
+    if st:
+        check("dl_conv_prompt", st)
 
 
 def dl_conv_step(x, w, bias, state, slot, y, silu: bool = True, status=None, stream=None) -> None:
     """The convolution of one new token per sequence: x, y [B, channels], slot [B] int32 or None."""
-    cv, xp, xs, B, sp, P, yp = _conv(x, w, bias, state, y, silu)
-    _same_device(x, w, bias, state, slot, y, status)
-    st = load().dl_conv_step(ctypes.byref(cv), xp, xs, B, sp, P, _index(slot, "slot", B, True),
-                             _index(status, "status", 1, True), yp, _stream(stream))
-    check("dl_conv_step", st)
+    dev = _device() if x.is_cuda else -2
+    cv, xp, xs, B, sp, P, yp = _conv(x, w, bias, state, y, silu, dev)
+    st = load().dl_conv_step(ctypes.byref(cv), xp, xs, B, sp, P, _index(slot, "slot", B, dev),
+                             _index(status, "status", 1, dev), yp, _raw_stream(stream, dev))
+    if st:
+        check("dl_conv_step", st)
 
 
-def _ssm(S, x, dt, A, b, c, y, D, dt_bias, z):
-    P, H, dk, dv = _dims(S)
-    if x.dim() != 3 or b.dim() != 3:
-        raise ValueError("x must be [rows, H, d_v], b and c [rows, G, d_k]")
-    f32 = _torch().float32
+def _ssm(S, x, dt, A, b, c, y, D, dt_bias, z, dev):
+    if x.dim() != 3 or b.dim() != 3 or S.dim() != 4:
+        raise ValueError("S must be [P, H, d_v, d_k], x [rows, H, d_v], b and c [rows, G, d_k]")
+    P, H, dv, dk = S.shape
     rows, G = x.shape[0], b.shape[1]
-    code = _in_dtype(x, dt, b, c, y, z)
-    zp, zs = _rows(z, "z", (rows, H, dv)) if z is not None else (None, 0)
-    m = dl_ssm(*_rows(x, "x", (rows, H, dv)), *_rows(dt, "dt", (rows, H)), *_rows(b, "b", (rows, G, dk)),
-               *_rows(c, "c", (rows, G, dk)), zp, zs, _full(A, "A", (H,), f32), _full(D, "D", (H,), f32, True),
-               _full(dt_bias, "dt_bias", (H,), f32, True), code)
-    return m, P, H, G, dk, dv, rows, _full(y, "y", (rows, H, dv))
+    wide, keys, heads = (rows, H, dv), (rows, G, dk), (H,)
+    zp, zs = (None, 0) if z is None else _rows(z, "z", wide, dev)
+    xp, xs = _rows(x, "x", wide, dev)
+    tp, ts = _rows(dt, "dt", (rows, H), dev)
+    bp, bs = _rows(b, "b", keys, dev)
+    cp, cs = _rows(c, "c", keys, dev)
+    if A is None:
+        raise ValueError("A is required")
+    m = dl_ssm(xp, xs, tp, ts, bp, bs, cp, cs, zp, zs, _f32(A, "A", heads, dev), _f32(D, "D", heads, dev),
+               _f32(dt_bias, "dt_bias", heads, dev), _float_code(x, dt, b, c, y, z))
+    return m, P, H, G, dk, dv, rows, _full(y, "y", wide, dev), _full(S, "S", S.shape, dev), _float_code(S)
 
 
 def dl_ssm_work_bytes(T: int, n_seq: int, H: int, d_k: int, d_v: int) -> int:
@@ -619,21 +665,24 @@ def dl_ssm_prompt(S, seq_start, slot, x, dt, A, b, c, y, D=None, dt_bias=None, z
     [T, H], b, c [T, G, d_k] (rows may be strided; y is contiguous), A, D, dt_bias
     [H] float32, seq_start [n + 1] int32, slot [n] int32 or None, work a tensor of
     dl_ssm_work_bytes(T, n, H, d_k, d_v) bytes."""
-    m, P, H, G, dk, dv, T, yp = _ssm(S, x, dt, A, b, c, y, D, dt_bias, z)
+    dev = _device() if x.is_cuda else -2
+    m, P, H, G, dk, dv, T, yp, Sp, sc = _ssm(S, x, dt, A, b, c, y, D, dt_bias, z, dev)
     n = seq_start.numel() - 1
-    wp, wb = (_ptr(work, "work"), work.numel() * work.element_size()) if work is not None and work.numel() else (None, 0)
-    _same_device(S, seq_start, slot, x, dt, A, b, c, y, D, dt_bias, z, work, status)
-    st = load().dl_ssm_prompt(_ptr(S, "S"), _dtype_code(S), P, _index(slot, "slot", n, True),
-                              _index(status, "status", 1, True), ctypes.byref(m),
-                              _index(seq_start, "seq_start", n + 1, False), n, T, yp, H, G, dk, dv, wp, wb,
-                              _stream(stream))
-    check("dl_ssm_prompt", st)
+    wp, wb = None, 0
+    if work is not None and work.numel():
+        wp, wb = _full(work, "work", work.shape, dev), work.numel() * work.element_size()
+    st = load().dl_ssm_prompt(Sp, sc, P, _index(slot, "slot", n, dev), _index(status, "status", 1, dev), ctypes.byref(m),
+                              _index(seq_start, "seq_start", n + 1, dev), n, T, yp, H, G, dk, dv, wp, wb,
+                              _raw_stream(stream, dev))
+    if st:
+        check("dl_ssm_prompt", st)
 
 
 def dl_ssm_step(S, slot, x, dt, A, b, c, y, D=None, dt_bias=None, z=None, status=None, stream=None) -> None:
     """The scan of one new token per sequence: x, y (z) [B, H, d_v], dt [B, H], b, c [B, G, d_k], slot [B] int32 or None."""
-    m, P, H, G, dk, dv, B, yp = _ssm(S, x, dt, A, b, c, y, D, dt_bias, z)
-    _same_device(S, slot, x, dt, A, b, c, y, D, dt_bias, z, status)
-    st = load().dl_ssm_step(_ptr(S, "S"), _dtype_code(S), P, _index(slot, "slot", B, True),
-                            _index(status, "status", 1, True), ctypes.byref(m), yp, B, H, G, dk, dv, _stream(stream))
-    check("dl_ssm_step", st)
+    dev = _device() if x.is_cuda else -2
+    m, P, H, G, dk, dv, B, yp, Sp, sc = _ssm(S, x, dt, A, b, c, y, D, dt_bias, z, dev)
+    st = load().dl_ssm_step(Sp, sc, P, _index(slot, "slot", B, dev), _index(status, "status", 1, dev), ctypes.byref(m), yp, B, H,
+                            G, dk, dv, _raw_stream(stream, dev))
+    if st:
+        check("dl_ssm_step", st)

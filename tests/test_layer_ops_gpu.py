@@ -140,6 +140,28 @@ def test_norm_without_rows(g):
     g.dl_rms_norm(e, torch.ones(64, device="cuda"), 1e-5, e.clone())
 
 
+def test_binding_refuses_what_does_not_fit(g):
+    x, w, h = torch.zeros(2, 64, device="cuda"), torch.zeros(64, device="cuda"), torch.zeros(2, 64)
+    q = torch.zeros(2, 64, dtype=torch.int8, device="cuda")
+    bad = [(ValueError, "8-bit y", lambda: g.dl_rms_norm(x, w, 1e-5, q)),
+           (ValueError, "go together", lambda: g.dl_rms_norm(x, w, 1e-5, x.clone(), residual=x)),
+           (ValueError, "scale has", lambda: g.dl_rms_norm(x, w, 1e-5, q, scale=w)),
+           (TypeError, "float32", lambda: g.dl_rms_norm(x, w, 1e-5, q, scale=torch.zeros(2, dtype=BF16, device="cuda"))),
+           (ValueError, "CUDA tensor", lambda: g.dl_rms_norm(x, w, 1e-5, h)),
+           (ValueError, "contiguous", lambda: g.dl_rms_norm(x.t(), w[:2], 1e-5, torch.zeros(64, 2, device="cuda"))),
+           (TypeError, "unsupported", lambda: g.dl_rms_norm(x.half(), w, 1e-5, x.clone())),
+           (TypeError, "share one dtype", lambda: g.dl_conv_step(x, torch.zeros(64, 4, device="cuda", dtype=BF16), None,
+                                                                 torch.zeros(2, 3, 64, device="cuda"), None, x.clone())),
+           (TypeError, "int32", lambda: g.dl_conv_step(x, torch.zeros(64, 4, device="cuda"), None, torch.zeros(2, 3, 64, device="cuda"),
+                                                       torch.zeros(2, dtype=torch.int64, device="cuda"), x.clone())),
+           (ValueError, "state must be", lambda: g.dl_conv_step(x, torch.zeros(64, 4, device="cuda"), None,
+                                                                torch.zeros(2, 2, 64, device="cuda"), None, x.clone())),
+           (g.DeltaLogError, "overlaps", lambda: g.dl_rms_norm(x, w, 1e-5, x))]
+    for kind, text, call in bad:
+        with pytest.raises(kind, match=text):
+            call()
+
+
 # ------------------------------------------------------------------ convolution
 
 def starts(lens, first=0):
