@@ -456,7 +456,7 @@ static dl_status conv(const dl_conv *cv, const void *x, long long x_stride, int 
     Buf b[8];
     dl_status s = seq_checks(seq_start, ragged, n_seq, T, P, slot, status, b);
     if (s != DL_OK) return s;
-    if (((long long)T / 32 + n_seq) * cv->channels > (1LL << 38))
+    if (((long long)T / 8 + n_seq) * cv->channels > (1LL << 38))
         return fail(DL_ERR_UNSUPPORTED, "T * channels exceeds the launch limit");
     if (T == 0) return ok();
     const size_t es = elem_size(cv->dtype), C = cv->channels;

@@ -3,10 +3,15 @@
 //
 //   y_t[c] = act(bias[c] + sum_{j < K} w[c, j] x_{t-K+1+j}[c])
 //
-// HBM-bound (2 K + 5 operations per element moved twice): every input and
-// output moves once. A thread owns 16 bytes of channels and walks TT tokens
-// with the K - 1 inputs before them in registers, so an input is loaded once
-// and used K times; the loads of 8 tokens are issued before the first is used.
+// HBM-bound (2 K + 5 operations per element moved twice; the activation's two
+// special-function operations take three quarters of the copy's time): every
+// input and output moves once. A thread owns 16 bytes of channels and walks TT
+// tokens with the K - 1 inputs before them in registers, so an input is loaded
+// once and used K times. Its next 12 tokens are on the way to its own places in
+// shared memory (asynchronous copies that no other thread reads, so no
+// barriers): enough in flight without holding registers. With 8 tokens' loads
+// in registers instead, one block fitted an SM and 16263 tokens of 4352
+// channels took 106 us of a floor of 43.
 // A prompt's first tile reads its slot's history and also writes the new one
 // (the last K - 1 inputs, from x): no other thread reads that history, so the
 // update needs no second launch.
@@ -53,15 +58,105 @@ struct Filter {
                 for (int j = 0; j < K; ++j) w[e][j] = f[e * K + j];
         }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) bias[e] = p.bias ? to_f(static_cast<const T *>(p.bias)[ch + e]) : 0.f;
+        for (int e = 0; e < VEC; ++e) bias[e] = 0.f;
+        if (p.bias) {
+            const T *bp = static_cast<const T *>(p.bias) + ch;
+            if constexpr (VEC > 1) {
+                if (p.bias16)
+                    load_vec<VEC>(bp, bias);
+                else
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) bias[e] = to_f(bp[e]);
+            } else {
+                bias[0] = to_f(bp[0]);
+            }
+        }
     }
 };
 
+// act of pairs of sums, to the output's type.
+template <class T>
+__device__ __forceinline__ void finish_pair(T *out, uint64_t acc, bool silu) {
+    float a, b;
+    unpair(acc, a, b);
+    store_f(out, silu ? silu_f<T>(a) : a);
+    store_f(out + 1, silu ? silu_f<T>(b) : b);
+}
+template <class T>
+__device__ __forceinline__ uint64_t load_pair(const T *v) {
+    if constexpr (sizeof(T) == 2)
+        return pair_bf(*reinterpret_cast<const uint32_t *>(v));
+    else
+        return pair(v[0], v[1]);
+}
+
+// The wide path's walk over tokens t0 .. t1 - 1 of one thread's VEC channels:
+// x and y at the sequence's first row, `ring` the thread's places in shared
+// memory (RING of them, 256 apart), hist the K - 1 inputs before t0.
+constexpr int GROUP = 4, GROUPS = 3, RING = GROUP * GROUPS;  // tokens of one wait, waits in flight
+template <class T, int K, int VEC>
+__device__ __forceinline__ void walk_wide(const ConvParams &p, const T *x, T *y, int t0, int t1, uint4 *ring, int ch,
+                                          const RawV<T, VEC> (&hist)[K - 1]) {
+    constexpr int PAIRS = VEC / 2;
+    const int C = p.channels;
+    auto fetch = [&](int g) {  // the g-th GROUP of tokens
+#pragma unroll
+        for (int u = 0; u < GROUP; ++u) {
+            const int t = t0 + g * GROUP + u;
+            if (t < t1) cp_async16(ring + ((g % GROUPS) * GROUP + u) * 256, x + (long long)t * p.x_stride);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int g = 0; g < GROUPS - 1; ++g) fetch(g);
+    uint64_t w[PAIRS][K], bias[PAIRS], win[K - 1 + GROUP][PAIRS];
+    {
+        Filter<T, K, VEC> f;
+        f.load(p, ch);
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) {
+            bias[e] = pair(f.bias[2 * e], f.bias[2 * e + 1]);
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[e][j] = pair(f.w[2 * e][j], f.w[2 * e + 1][j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < PAIRS; ++e) win[j][e] = load_pair(&hist[j].v[2 * e]);
+    int g = 0;
+    for (int t = t0; t < t1; t += GROUP, ++g) {
+        fetch(g + GROUPS - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(GROUPS - 1) : "memory");
+#pragma unroll
+        for (int u = 0; u < GROUP; ++u) {
+            if (t + u < t1) {
+                RawV<T, VEC> in, out;
+                *reinterpret_cast<uint4 *>(in.v) = ring[((g % GROUPS) * GROUP + u) * 256];
+#pragma unroll
+                for (int e = 0; e < PAIRS; ++e) {
+                    win[K - 1 + u][e] = load_pair(&in.v[2 * e]);
+                    uint64_t acc = bias[e];
+#pragma unroll
+                    for (int j = 0; j < K; ++j) acc = fma2(w[e][j], win[u + j][e], acc);
+                    finish_pair(&out.v[2 * e], acc, p.silu);
+                }
+                out.store(y + (long long)(t + u) * C);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) win[j][e] = win[GROUP + j][e];
+    }
+}
+
 template <class T, int K, int VEC, int TT>
-__global__ void __launch_bounds__(256) conv_prompt_kernel(const ConvParams p, const SeqIdx q, int nv) {
+__global__ void __launch_bounds__(256, VEC > 1 ? 2 : 1) conv_prompt_kernel(const ConvParams p, const SeqIdx q, int nv) {
     using R = RawV<T, VEC>;
-    constexpr int U = 8;  // tokens whose loads are in flight
+    constexpr int U = 8;  // tokens whose loads are in flight (VEC = 1)
     static_assert(TT % U == 0 && TT >= K, "tile");
+    extern __shared__ uint4 ring[];
     const long long gid = (long long)blockIdx.x * 256 + threadIdx.x;
     if (gid < q.n_seq) seq_check(q, (int)gid);
     const long long tile = gid / nv;
@@ -75,7 +170,6 @@ __global__ void __launch_bounds__(256) conv_prompt_kernel(const ConvParams p, co
     const int t0 = in_seq * TT, t1 = min(t0 + TT, n), C = p.channels;
     const T *x = static_cast<const T *>(p.x) + (long long)s0 * p.x_stride + ch;
     T *y = static_cast<T *>(p.y) + (long long)s0 * C + ch;
-    Filter<T, K, VEC> f;
     R hist[K - 1];
     if (t0 == 0) {
         T *st = static_cast<T *>(p.state) + (long long)slot * (K - 1) * C + ch;
@@ -98,36 +192,30 @@ __global__ void __launch_bounds__(256) conv_prompt_kernel(const ConvParams p, co
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) hist[j].load(x + (long long)(t0 - (K - 1) + j) * p.x_stride);
     }
-    f.load(p, ch);
-    float win[K - 1 + U][VEC];
+    if constexpr (VEC > 1) {
+        walk_wide<T, K, VEC>(p, x, y, t0, t1, ring + threadIdx.x, ch, hist);
+    } else {
+        Filter<T, K, 1> f;
+        f.load(p, ch);
+        float win[K - 1 + U];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j)
+        for (int j = 0; j < K - 1; ++j) win[j] = to_f(hist[j].v[0]);
+        for (int t = t0; t < t1; t += U) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) win[j][e] = to_f(hist[j].v[e]);
-    for (int t = t0; t < t1; t += U) {
-        R raw[U];
+            for (int u = 0; u < U; ++u)
+                if (t + u < t1) win[K - 1 + u] = to_f(x[(long long)(t + u) * p.x_stride]);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < t1) raw[u].load(x + (long long)(t + u) * p.x_stride);
+            for (int u = 0; u < U; ++u) {
+                if (t + u < t1) {
+                    float acc = f.bias[0];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u < t1) {
-                R out;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    win[K - 1 + u][e] = to_f(raw[u].v[e]);
-                    float acc = f.bias[e];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) acc = fmaf(f.w[e][j], win[u + j][e], acc);
-                    store_f(&out.v[e], p.silu ? silu_f<T>(acc) : acc);
+                    for (int j = 0; j < K; ++j) acc = fmaf(f.w[0][j], win[u + j], acc);
+                    store_f(y + (long long)(t + u) * C, p.silu ? silu_f<T>(acc) : acc);
                 }
-                out.store(y + (long long)(t + u) * C);
             }
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) win[j] = win[U + j];
         }
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) win[j][e] = win[U + j][e];
     }
 }
 
@@ -161,7 +249,11 @@ __global__ void __launch_bounds__(256) conv_step_kernel(const ConvParams p, cons
     out.store(static_cast<T *>(p.y) + row * C + ch);
 }
 
-constexpr int TT = 32;  // tokens a thread walks
+// Tokens a thread walks: 32 where that leaves every SM full (each tile reads its
+// K - 1 rows of history again), 8 in smaller calls, whose time is a chain of
+// loads (776 tokens of 1541 channels: 11.6 us by 32, FILL_ODD8 by 8).
+constexpr int TT_LONG = 32, TT_SHORT = 8;
+constexpr long long FILL = 148 * 2 * 256;
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -188,18 +280,31 @@ cudaError_t dispatch_conv(const ConvParams &p, F &&f) {
 
 }  // namespace
 
-cudaError_t launch_conv_prompt(const ConvParams &p, const SeqIdx &q, cudaStream_t st) {
+cudaError_t launch_conv_prompt(const ConvParams &conv, const SeqIdx &q, cudaStream_t st) {
+    ConvParams p = conv;
+    p.bias16 = aligned16(p.bias);
     return dispatch_conv(p, [&](auto t, auto k, auto vec) -> cudaError_t {
         using T = decltype(t);
         constexpr int K = decltype(k)::value, V = decltype(vec)::value;
         const int nv = p.channels / V;
-        const long long threads = ((long long)q.T / TT + q.n_seq) * nv;
-        conv_prompt_kernel<T, K, V, TT><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(p, q, nv);
-        return cudaGetLastError();
+        auto go = [&](auto tt) -> cudaError_t {
+            constexpr int TT = decltype(tt)::value;
+            const long long threads = ((long long)q.T / TT + q.n_seq) * nv;
+            const size_t smem = V > 1 ? RING * 256 * sizeof(uint4) : 0;
+            auto kern = conv_prompt_kernel<T, K, V, TT>;
+            const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), smem);
+            if (e != cudaSuccess) return e;
+            kern<<<(unsigned)((threads + 255) / 256), 256, smem, st>>>(p, q, nv);
+            return cudaGetLastError();
+        };
+        if ((long long)q.T / TT_LONG * nv >= FILL) return go(std::integral_constant<int, TT_LONG>{});
+        return go(std::integral_constant<int, TT_SHORT>{});
     });
 }
 
-cudaError_t launch_conv_step(const ConvParams &p, const SeqIdx &q, cudaStream_t st) {
+cudaError_t launch_conv_step(const ConvParams &conv, const SeqIdx &q, cudaStream_t st) {
+    ConvParams p = conv;
+    p.bias16 = aligned16(p.bias);
     return dispatch_conv(p, [&](auto t, auto k, auto vec) -> cudaError_t {
         using T = decltype(t);
         constexpr int K = decltype(k)::value, V = decltype(vec)::value;

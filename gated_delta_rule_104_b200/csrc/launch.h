@@ -157,6 +157,7 @@ struct ConvParams {
     int channels, taps;
     dl_dtype dt;
     bool silu;
+    bool bias16 = false;  // bias is 16-byte aligned (set by the launch)
 };
 cudaError_t launch_conv_prompt(const ConvParams &p, const SeqIdx &q, cudaStream_t st);
 cudaError_t launch_conv_step(const ConvParams &p, const SeqIdx &q, cudaStream_t st);

@@ -260,9 +260,9 @@ rows_from_8bit_kernel(const uint8_t *__restrict__ codes, const float *__restrict
         row = i / per_row;
     const int col = (int)(i - row * per_row) * VEC;
     const float s = scale[row * groups + (group ? col / group : 0)];
-    uint8_t raw[VEC];
-    if constexpr (VEC == 8)
-        *reinterpret_cast<uint2 *>(raw) = __ldcs(reinterpret_cast<const uint2 *>(codes + i * VEC));
+    alignas(16) uint8_t raw[VEC];
+    if constexpr (VEC == 16)
+        *reinterpret_cast<uint4 *>(raw) = __ldcs(reinterpret_cast<const uint4 *>(codes + i * VEC));
     else
         raw[0] = codes[i];
     float x[VEC];
@@ -317,8 +317,8 @@ cudaError_t launch_rms_norm(const NormParams &p, cudaStream_t st) {
 
 cudaError_t launch_rows_from_8bit(const void *codes, dl_dtype c_dt, const float *scale, int group, void *out,
                                   dl_dtype out_dt, long long rows, int width, cudaStream_t st) {
-    const bool i8 = c_dt == DL_I8, wide = width % 8 == 0 && aligned(codes, 8) && aligned(out, 16);
-    const int per_row = wide ? width / 8 : width, groups = group ? (width + group - 1) / group : 1;
+    const bool i8 = c_dt == DL_I8, wide = width % 16 == 0 && aligned(codes, 16) && aligned(out, 16);
+    const int per_row = wide ? width / 16 : width, groups = group ? (width + group - 1) / group : 1;
     const long long chunks = rows * per_row;
     const unsigned blocks = (unsigned)((chunks + 255) / 256);
     const uint8_t *c = static_cast<const uint8_t *>(codes);
@@ -326,7 +326,7 @@ cudaError_t launch_rows_from_8bit(const void *codes, dl_dtype c_dt, const float 
         using OT = decltype(o);
         OT *dst = static_cast<OT *>(out);
         if (wide)
-            rows_from_8bit_kernel<OT, 8><<<blocks, 256, 0, st>>>(c, scale, dst, chunks, per_row, groups, group, i8);
+            rows_from_8bit_kernel<OT, 16><<<blocks, 256, 0, st>>>(c, scale, dst, chunks, per_row, groups, group, i8);
         else
             rows_from_8bit_kernel<OT, 1><<<blocks, 256, 0, st>>>(c, scale, dst, chunks, per_row, groups, group, i8);
         return cudaGetLastError();

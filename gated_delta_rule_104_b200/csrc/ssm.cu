@@ -20,13 +20,15 @@ __device__ __forceinline__ void step_size(const dl_ssm &in, long long row, int h
     da = expf(dt * in.A[h]);
 }
 
+constexpr int STEP_R = 8;  // state loads a lane has in flight
+
 // One token per sequence. HBM-bound on the state like the eager step, and laid
 // out as that is: a state row over a group of lanes, 16 bytes each, R = 4 rows'
 // loads in flight per lane before any arithmetic, a shuffle sum per row, no
 // shared memory.
 template <class ST, class IT, int DK>
 __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p, const SeqIdx q, long long num_units) {
-    constexpr int VEC = StateVec<ST>::N, G = DK / VEC, RPW = 32 / G, R = 4, UNIT = R * RPW;
+    constexpr int VEC = StateVec<ST>::N, G = DK / VEC, RPW = 32 / G, R = STEP_R, UNIT = R * RPW;
     const long long gid = (long long)blockIdx.x * 256 + threadIdx.x;
     if (gid < q.n_seq) seq_check(q, (int)gid);
     const int lane = threadIdx.x & 31;
@@ -217,7 +219,7 @@ cudaError_t launch_ssm_step(const SsmParams &p, const SeqIdx &q, cudaStream_t st
     return dispatch_ssm(p, [&](auto s, auto t, auto dk) -> cudaError_t {
         using ST = decltype(s);
         using IT = decltype(t);
-        constexpr int DK = decltype(dk)::value, UNIT = 4 * 32 / (DK / StateVec<ST>::N);
+        constexpr int DK = decltype(dk)::value, UNIT = STEP_R * 32 / (DK / StateVec<ST>::N);
         static_assert(64 % UNIT == 0, "a unit is rows of one head");
         const long long units = (long long)q.n_seq * p.H * (p.dv / UNIT);
         ssm_step_kernel<ST, IT, DK><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(p, q, units);
