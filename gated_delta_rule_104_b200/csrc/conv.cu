@@ -74,13 +74,15 @@ struct Filter {
     }
 };
 
-// act of pairs of sums, to the output's type.
-template <class T>
-__device__ __forceinline__ void finish_pair(T *out, uint64_t acc, bool silu) {
-    float a, b;
-    unpair(acc, a, b);
-    store_f(out, silu ? silu_f<T>(a) : a);
-    store_f(out + 1, silu ? silu_f<T>(b) : b);
+// act of a pair of sums, to the output's type.
+template <class T, bool SILU>
+__device__ __forceinline__ void finish_pair(T *out, uint64_t acc) {
+    if constexpr (SILU) acc = silu2<T>(acc);
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint32_t *>(out) = pack_bf2(acc);
+    } else {
+        unpair(acc, out[0], out[1]);
+    }
 }
 template <class T>
 __device__ __forceinline__ uint64_t load_pair(const T *v) {
@@ -94,7 +96,7 @@ __device__ __forceinline__ uint64_t load_pair(const T *v) {
 // x and y at the sequence's first row, `ring` the thread's places in shared
 // memory (RING of them, 256 apart), hist the K - 1 inputs before t0.
 constexpr int GROUP = 4, GROUPS = 3, RING = GROUP * GROUPS;  // tokens of one wait, waits in flight
-template <class T, int K, int VEC>
+template <class T, int K, int VEC, bool SILU>
 __device__ __forceinline__ void walk_wide(const ConvParams &p, const T *x, T *y, int t0, int t1, uint4 *ring, int ch,
                                           const RawV<T, VEC> (&hist)[K - 1]) {
     constexpr int PAIRS = VEC / 2;
@@ -139,7 +141,7 @@ __device__ __forceinline__ void walk_wide(const ConvParams &p, const T *x, T *y,
                     uint64_t acc = bias[e];
 #pragma unroll
                     for (int j = 0; j < K; ++j) acc = fma2(w[e][j], win[u + j][e], acc);
-                    finish_pair(&out.v[2 * e], acc, p.silu);
+                    finish_pair<T, SILU>(&out.v[2 * e], acc);
                 }
                 out.store(y + (long long)(t + u) * C);
             }
@@ -193,7 +195,10 @@ __global__ void __launch_bounds__(256, VEC > 1 ? 2 : 1) conv_prompt_kernel(const
         for (int j = 0; j < K - 1; ++j) hist[j].load(x + (long long)(t0 - (K - 1) + j) * p.x_stride);
     }
     if constexpr (VEC > 1) {
-        walk_wide<T, K, VEC>(p, x, y, t0, t1, ring + threadIdx.x, ch, hist);
+        if (p.silu)
+            walk_wide<T, K, VEC, true>(p, x, y, t0, t1, ring + threadIdx.x, ch, hist);
+        else
+            walk_wide<T, K, VEC, false>(p, x, y, t0, t1, ring + threadIdx.x, ch, hist);
     } else {
         Filter<T, K, 1> f;
         f.load(p, ch);

@@ -176,12 +176,36 @@ cudaError_t launch_ssm_tc(const SsmParams &p, const SeqIdx &q, void *work, cudaS
 cudaError_t read_ssm_faults(unsigned int *out, bool clear);
 size_t ssm_work_bytes(int T, int n_seq, int H, int dk, int dv);
 
-// u / (1 + exp(-u)): the fast exponential and division where the result is
-// rounded to bf16, the accurate ones otherwise.
+__device__ __forceinline__ float ex2_ftz(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+// u / (1 + exp(-u)): by the hardware's exponential and reciprocal where the
+// result is rounded to bf16, the accurate ones otherwise.
 template <class T>
 __device__ __forceinline__ float silu_f(float u) {
-    if constexpr (sizeof(T) == 2) return __fdividef(u, 1.f + __expf(-u));
+    if constexpr (sizeof(T) == 2) return u * rcp_ftz(1.f + ex2_ftz(-LOG2E * u));
     return u / (1.f + expf(-u));
+}
+// The same of a pair.
+template <class T>
+__device__ __forceinline__ uint64_t silu2(uint64_t u) {
+    float a, b;
+    if constexpr (sizeof(T) == 2) {
+        unpair(mul2(u, pair(-LOG2E, -LOG2E)), a, b);
+        unpair(fma2(pair(ex2_ftz(a), ex2_ftz(b)), pair(1.f, 1.f), pair(1.f, 1.f)), a, b);
+        return mul2(u, pair(rcp_ftz(a), rcp_ftz(b)));
+    } else {
+        unpair(u, a, b);
+        return pair(silu_f<T>(a), silu_f<T>(b));
+    }
 }
 __device__ __forceinline__ float softplus_f(float u) { return fmaxf(u, 0.f) + log1pf(expf(-fabsf(u))); }
 __device__ __forceinline__ void store_f(float *p, float x) { *p = x; }

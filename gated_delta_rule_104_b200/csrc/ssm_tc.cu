@@ -56,7 +56,6 @@ namespace {
 
 using namespace stc;
 
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr int SMS = 148;  // of a B200: the workspace's size must not depend on the device
 
 struct Args {
@@ -154,11 +153,6 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t addr, const uint32_t (&r)[
                  "r"(r[3])
                  : "memory");
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 // Folds a pair of bfloat16 into `acc`, which turns NaN if one of them is no finite number.
 __device__ __forceinline__ void watch(uint32_t &acc, uint32_t pair) {
     asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(pair), "r"(0u));
@@ -222,12 +216,14 @@ __device__ __forceinline__ void store_row16(bf16 *p, const uint32_t (&v)[16]) {
 
 // Step sizes and decays of a chunk of one head, by one warp: lane = token of each 32.
 struct Steps {
-    float raw[4];  // dt_raw of tokens lane, 32 + lane, ..
+    float raw[4], ahead[4];  // dt_raw of tokens lane, 32 + lane, ..: this chunk's, and the next one's on its way
     // Rows row0 + ..; tokens at or behind `m` get no step.
     __device__ __forceinline__ void fetch(const dl_ssm &in, long long row0, int h, int lane, int m) {
 #pragma unroll
+        for (int j = 0; j < 4; ++j) raw[j] = ahead[j];
+#pragma unroll
         for (int j = 0; j < 4; ++j)
-            raw[j] = 32 * j + lane < m ? to_f(static_cast<const bf16 *>(in.dt)[(row0 + 32 * j + lane) * in.dt_stride + h]) : 0.f;
+            ahead[j] = 32 * j + lane < m ? to_f(static_cast<const bf16 *>(in.dt)[(row0 + 32 * j + lane) * in.dt_stride + h]) : 0.f;
     }
     // Every value of the chunk, before the place for it is free.
     float dt[4], l[4], u[4], w[4], end;
@@ -430,7 +426,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     const float *sc = scal(c, h);
                     const float lt = lth[h];
                     if (!diagonal) {
-                        const float v = exp2_fast(lt - sc[Scal::RB + (k >> 1)]);
+                        const float v = ex2_ftz(lt - sc[Scal::RB + (k >> 1)]);
                         const uint64_t vv = pair(v, v);
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
@@ -445,7 +441,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                         for (int e = 0; e < 16; e += 2) {
                             float x0, x1;
                             unpair(fma2(*reinterpret_cast<const uint64_t *>(sc + Scal::L + 16 * k + e), pair(-1.f, -1.f), ll), x0, x1);
-                            const uint64_t f = mul2(pair(exp2_fast(x0), exp2_fast(x1)),
+                            const uint64_t f = mul2(pair(ex2_ftz(x0), ex2_ftz(x1)),
                                                     *reinterpret_cast<const uint64_t *>(sc + Scal::DT + 16 * k + e));
                             pw[e / 2] = pack_bf2(mul2(pair(g[e], g[e + 1]), f)) & low_bits(upto - 16 * e);
                         }
@@ -483,6 +479,23 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             // reach behind the segment (or x holds what is no number)
             const int m = min(Q, len - c * Q);
             const long long row = (long long)row0 + c * Q + t;
+            // z / (1 + exp(-z)) of 16 value columns; the first before Y is there
+            uint64_t gate[GATE ? 8 : 1];
+            auto load_gate = [&](int k) {
+                const int zi = 4 * c + k;
+                if (!wait_warp(&bars[Z_FULL + 3 * zslot + zi % 3], (zi / 3) & 1, abort)) return false;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 z = *reinterpret_cast<const uint4 *>(sm + LY::z(zslot, zi % 3) + gate_off(lane, j));
+                    const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) gate[GATE ? 4 * j + e : 0] = silu2<bf16>(pair_bf(zw[e]));
+                }
+                __syncwarp();
+                load_z();
+                return true;
+            };
+            if (GATE && !load_gate(0)) break;
             if (!wait_warp(&bars[Y_DONE], par, abort)) break;
             tc::tc_fence_after();
             tc::tmem_ld16(trow + T_Y + 64 * half, r0);
@@ -496,50 +509,49 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             auto x_at = [&](int k, int j) {  // 8 of 16 value columns
                 return reinterpret_cast<uint4 *>(xp + lane * 128 + ((32 * k + 16 * j) ^ swz));
             };
-            auto columns = [&](auto direct_c) {
-                auto finish = [&](int k, const uint32_t (&y)[16], uint4 x0, uint4 x1) {
-                    const int zi = 4 * c + k;
-                    if (GATE && !wait_warp(&bars[Z_FULL + 3 * zslot + zi % 3], (zi / 3) & 1, abort)) return false;
+            auto columns = [&](int k, const uint32_t (&y)[16], const uint4 &x0, const uint4 &x1) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 xv = j ? x1 : x0;
-                        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-                        uint32_t zw[4] = {0u, 0u, 0u, 0u}, ow[4];
-                        if constexpr (GATE) {
-                            const uint4 zv = *reinterpret_cast<const uint4 *>(sm + LY::z(zslot, zi % 3) + gate_off(lane, j));
-                            zw[0] = zv.x, zw[1] = zv.y, zw[2] = zv.z, zw[3] = zv.w;
-                        }
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 xv = j ? x1 : x0;
+                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                    uint32_t ow[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint64_t o = fma2(DD, pair_bf(xw[e]), pair(y[8 * j + 2 * e], y[8 * j + 2 * e + 1]));
-                            if constexpr (GATE) o = mul2(o, pair(silu_f<bf16>(bf_lo(zw[e])), silu_f<bf16>(bf_hi(zw[e]))));
-                            ow[e] = pack_bf2(o);
-                        }
-                        const uint4 out = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-                        if constexpr (!decltype(direct_c)::value)
-                            *x_at(k, j) = out;
-                        else if (t < m && live)
-                            reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.y) + (row * p.H + yh) * p.dv + ycol)[2 * k + j] = out;
+                    for (int e = 0; e < 4; ++e) {
+                        uint64_t o = fma2(DD, pair_bf(xw[e]), pair(y[8 * j + 2 * e], y[8 * j + 2 * e + 1]));
+                        if constexpr (GATE) o = mul2(o, gate[4 * j + e]);
+                        ow[e] = pack_bf2(o);
                     }
-                    if constexpr (GATE) {
-                        __syncwarp();
-                        load_z();
-                    }
-                    return true;
-                };
+                    const uint4 out = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                    if (!direct)
+                        *x_at(k, j) = out;
+                    else if (t < m && live)
+                        reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.y) + (row * p.H + yh) * p.dv + ycol)[2 * k + j] = out;
+                }
+            };
+            if constexpr (GATE) {
+                bool ok = true;
 #pragma unroll 1
-                for (int k = 0; k < 4; k += 2) {  // 16 value columns each
+                for (int k = 0; k < 4; ++k) {  // 16 value columns each
+                    const uint4 xa = *x_at(k, 0), xb = *x_at(k, 1);
+                    tc::tmem_wait_ld();
+                    columns(k, r0, xa, xb);
+                    if (k == 3) break;
+                    tc::tmem_ld16(trow + T_Y + 64 * half + 16 * k + 16, r0);
+                    if (!(ok = load_gate(k + 1))) break;
+                }
+                if (!ok) break;
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < 4; k += 2) {
                     const uint4 xa = *x_at(k, 0), xb = *x_at(k, 1), xc = *x_at(k + 1, 0), xd = *x_at(k + 1, 1);
                     tc::tmem_wait_ld();
                     tc::tmem_ld16(trow + T_Y + 64 * half + 16 * k + 16, r1);
-                    if (!finish(k, r0, xa, xb)) return false;
+                    columns(k, r0, xa, xb);
                     tc::tmem_wait_ld();
                     if (k == 0) tc::tmem_ld16(trow + T_Y + 64 * half + 32, r0);
-                    if (!finish(k + 1, r1, xc, xd)) return false;
+                    columns(k + 1, r1, xc, xd);
                 }
-                return true;
-            };
-            if (!(direct ? columns(std::true_type{}) : columns(std::false_type{}))) break;
+            }
             tc::tc_fence_before();
             arrive(Y_FREE);
             if (!direct) {
@@ -604,7 +616,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 
             float ex[NH];
 #pragma unroll
-            for (int k = 0; k < NH; ++k) ex[k] = exp2_fast(scal(c, k)[Scal::L + r]);
+            for (int k = 0; k < NH; ++k) ex[k] = ex2_ftz(scal(c, k)[Scal::L + r]);
             arrive(SC_FREE + par);
             if (!(ok = wait_warp(&bars[Y2_DONE], par, abort))) break;
             tc::tc_fence_after();
@@ -826,8 +838,8 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         st.fetch(in, row0, rw.h0 + h, lane, live ? len : 0);
         for (int c = 0; c < chunks; ++c) {
             const int m = live ? len - c * Q : 0;
-            st.compute(bias, A, lane, m, 0.f);
             st.fetch(in, (long long)row0 + (c + 1) * Q, rw.h0 + h, lane, m - Q);
+            st.compute(bias, A, lane, m, 0.f);
             if (c >= 2 && !wait_warp(&bars[SC_FREE + (c & 1)], (uint32_t)((c >> 1) - 1) & 1, abort)) break;
             st.write(scal(c, h), lane);
             arrive(SC_FULL + (c & 1));
@@ -1002,9 +1014,9 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         st.fetch(in, (long long)row0 + (chunks - 1) * Q, rw.h0 + h, lane, m);
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
+            st.fetch(in, (long long)row0 + (chunks - 2 - c) * Q, rw.h0 + h, lane, c + 1 < chunks ? m : 0);
             st.compute(bias, A, lane, m, behind);
             behind += st.end;
-            st.fetch(in, (long long)row0 + (chunks - 2 - c) * Q, rw.h0 + h, lane, c + 1 < chunks ? m : 0);
             if (c >= 2 && !(ok = wait_warp(&bars[SC_FREE + (c & 1)], (uint32_t)((c >> 1) - 1) & 1, abort))) break;
 #pragma unroll
             for (int j = 0; j < 4; ++j) weights(c, h)[32 * j + lane] = st.w[j];
@@ -1039,17 +1051,27 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const Args a, long long q
     load_vec<4>(static_cast<const ST *>(p.S) + slot * per + at, s);
     float4 *e = reinterpret_cast<float4 *>(a.seg_state + base * per + at);
     const float *dec = a.seg_decay + base * p.H + h;
-    float4 next = *e;
-    for (int j = 0; j < segs; ++j, e += per / 4, dec += p.H) {
-        const float4 own = next;
-        if (j + 2 < segs) next = e[per / 4];
-        *e = make_float4(s[0], s[1], s[2], s[3]);
-        if (j + 1 == segs) break;
-        const float d = expf(*dec);
-        s[0] = fmaf(s[0], d, own.x);
-        s[1] = fmaf(s[1], d, own.y);
-        s[2] = fmaf(s[2], d, own.z);
-        s[3] = fmaf(s[3], d, own.w);
+    constexpr int AHEAD = 6;  // segments whose loads are in flight
+    for (int j0 = 0; j0 < segs; j0 += AHEAD) {
+        float4 own[AHEAD];
+        float d[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (j0 + j + 1 < segs) {
+                own[j] = e[(j0 + j) * (per / 4)];
+                d[j] = dec[(long long)(j0 + j) * p.H];
+            }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (j0 + j >= segs) break;
+            e[(j0 + j) * (per / 4)] = make_float4(s[0], s[1], s[2], s[3]);
+            if (j0 + j + 1 == segs) break;
+            const float f = expf(d[j]);
+            s[0] = fmaf(s[0], f, own[j].x);
+            s[1] = fmaf(s[1], f, own[j].y);
+            s[2] = fmaf(s[2], f, own[j].z);
+            s[3] = fmaf(s[3], f, own[j].w);
+        }
     }
 }
 
