@@ -214,16 +214,38 @@ __device__ __forceinline__ void store_row16(bf16 *p, const uint32_t (&v)[16]) {
     reinterpret_cast<uint4 *>(p)[1] = pack8(v + 8);
 }
 
+// Tile k of at most 32 sequences taken from the longest to the shortest (by a
+// whole warp): its sequence, or -1, and the segment in it. Blocks start in this
+// order, so the short ones fill in behind the long ones. (Prompts of 17 to 5000
+// tokens on 32 heads: BY_LENGTH us; 182 in the sequences' own order.)
+__device__ __forceinline__ int tile_by_length(const SeqIdx &q, int k, int len, int lane, int &seg) {
+    int s0, n = -1, first = 0;
+    if (lane < q.n_seq) seq_range(q, lane, s0, n);
+    const int segs = n > 0 ? segs_of(n, len) : 0;
+    for (int j = 0; j < q.n_seq; ++j) {
+        const int n_j = __shfl_sync(0xffffffffu, n, j), segs_j = __shfl_sync(0xffffffffu, segs, j);
+        if (n_j > n || (n_j == n && j < lane)) first += segs_j;
+    }
+    const unsigned mine = __ballot_sync(0xffffffffu, first <= k && k < first + segs);
+    if (!mine) return -1;
+    const int i = __ffs(mine) - 1;
+    seg = k - __shfl_sync(0xffffffffu, first, i);
+    return i;
+}
+
 // Step sizes and decays of a chunk of one head, by one warp: lane = token of each 32.
 struct Steps {
-    float raw[4], ahead[4];  // dt_raw of tokens lane, 32 + lane, ..: this chunk's, and the next one's on its way
+    // dt_raw of tokens lane, 32 + lane, ..: this chunk's, and the next one's on its way (as
+    // loaded: a conversion would wait for it)
+    float raw[4];
+    unsigned short ahead[4];
     // Rows row0 + ..; tokens at or behind `m` get no step.
     __device__ __forceinline__ void fetch(const dl_ssm &in, long long row0, int h, int lane, int m) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) raw[j] = ahead[j];
+        for (int j = 0; j < 4; ++j) raw[j] = bf_lo(ahead[j]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            ahead[j] = 32 * j + lane < m ? to_f(static_cast<const bf16 *>(in.dt)[(row0 + 32 * j + lane) * in.dt_stride + h]) : 0.f;
+            ahead[j] = 32 * j + lane < m ? static_cast<const unsigned short *>(in.dt)[(row0 + 32 * j + lane) * in.dt_stride + h] : 0;
     }
     // Every value of the chunk, before the place for it is free.
     float dt[4], l[4], u[4], w[4], end;
@@ -326,7 +348,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     const int tile = (int)(blockIdx.x / (unsigned)a.units);
     const Rows rw = rows_of<NH>(p, (int)(blockIdx.x - (unsigned)tile * a.units));
     int seg = 0, s0, n;
-    const int i = seq_of_tile(a.q, tile, a.seg_len, seg);
+    const int i = a.q.n_seq <= 32 ? tile_by_length(a.q, tile, a.seg_len, lane, seg) : seq_of_tile(a.q, tile, a.seg_len, seg);
     if (i < 0 || !seq_range(a.q, i, s0, n)) return;
     const int slot = seq_slot(a.q, i);
     const int segs = segs_of(n, a.seg_len);
@@ -857,7 +879,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 // last to the first, so that each token's weight takes in the decay behind its
 // chunk and the state needs no scaling. Three parts always: what is summed here
 // reaches the last state.
-constexpr int END_THREADS = 384;
+constexpr int END_THREADS = 640;  // 16 warps on W, three chunks ahead of the products: what bounds this is W
 
 template <int DK, int NH>
 __global__ void __launch_bounds__(END_THREADS, 1)
@@ -865,7 +887,7 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                    const __grid_constant__ Args a) {
     using LY = EndLayout<DK, NH>;
     constexpr int TERMS = 3;
-    enum { B_FULL, FREE = B_FULL + 2, X_FULL = FREE + 2, SC_FULL = X_FULL + 2, SC_FREE = SC_FULL + 2, W_FULL = SC_FREE + 2,
+    enum { B_FULL, FREE = B_FULL + LY::ST, X_FULL = FREE + LY::ST, SC_FULL = X_FULL + LY::ST, SC_FREE = SC_FULL + 2, W_FULL = SC_FREE + 2,
            W_FREE = W_FULL + 8, DONE = W_FREE + 8, BARS };  // (a place of W for each 16 tokens of a chunk)
     constexpr int T_W8 = 256;
     static_assert(LY::N_BAR == BARS, "barriers");
@@ -893,12 +915,12 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     if (tid == 0) {
         for (int b = 0; b < BARS; ++b) {
             const bool sc_full = b >= SC_FULL && b < SC_FREE, sc_free = b >= SC_FREE && b < W_FULL, w_full = b >= W_FULL && b < W_FREE;
-            tc::mbar_init(&bars[b], sc_full ? NH : sc_free ? 8 : w_full ? 4 : 1);
+            tc::mbar_init(&bars[b], sc_full ? NH : sc_free ? 16 : w_full ? 4 : 1);
         }
         *abort = 0;
         tc::mbar_init_fence();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tc::tmem_alloc(tslot, T_COLS);
         tc::tmem_relinquish();
     }
@@ -911,26 +933,28 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         if (lane == 0) tc::mbar_arrive(&bars[b]);
     };
 
-    if (warp < 8) {
-        // ------------------------------------------------ W, every other 32 tokens; the end state (thread = value row r)
+    if (warp < 16) {
+        // ------------------------------------------------ W, 16 of each 64 tokens; the end state (thread = value row r)
         const int quad = warp & 3, set = warp >> 2, r = 32 * quad + lane, h = NH == 2 ? r >> 6 : 0;
         const uint32_t trow = tb + ((uint32_t)(32 * quad) << 16);
         bool ok = true;
         for (int c = 0; ok && c < chunks; ++c) {
             const uint32_t par = c & 1, par2 = (c >> 1) & 1;
-            if (!(ok = wait_warp(&bars[X_FULL + par], par2, abort) && wait_warp(&bars[SC_FULL + par], par2, abort))) break;
+            const int k = c % LY::ST;
+            if (!(ok = wait_warp(&bars[X_FULL + k], (uint32_t)(c / LY::ST) & 1, abort) && wait_warp(&bars[SC_FULL + par], par2, abort)))
+                break;
             const float *w = weights(c, h);
 #pragma unroll 1
-            for (int g = set; g < 8; g += 2) {  // 16 tokens
+            for (int g = set; g < 8; g += 4) {  // 16 tokens
                 if (c > 0) {
                     if (!(ok = wait_warp(&bars[W_FREE + g], (uint32_t)(c - 1) & 1, abort))) break;
                     tc::tc_fence_after();
                 }
                 uint32_t acc = 0u;
-                const uint32_t at = trow + T_W8 + W_PLACE * g, x16 = tc::smem_u32(sm + LY::x(par, g >> 1)) + 16 * 128 * (g & 1);
+                const uint32_t at = trow + T_W8 + W_PLACE * g, x16 = tc::smem_u32(sm + LY::x(k, g >> 1)) + 16 * 128 * (g & 1);
                 convert_w<TERMS, false>(at, x16, w + 16 * g, quad, lane, acc);
                 if (__any_sync(0xffffffffu, saw_no_number(acc))) convert_w<TERMS, true>(at, x16, w + 16 * g, quad, lane, acc);
-                if (g >= 6) arrive(SC_FREE + par);
+                if (g >= 4) arrive(SC_FREE + par);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 arrive(W_FULL + g);
@@ -949,15 +973,15 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             }
             tc::tc_fence_before();
         }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ------------------------------------------------ loads, from the last chunk
         if (lane == 0) {
             tc::tma_prefetch_desc(&map_x);
             tc::tma_prefetch_desc(&map_b);
             int issued = 0;
             for (int c = 0; c < chunks; ++c) {
-                const int k = c & 1, row = row0 + (chunks - 1 - c) * Q;
-                if (c >= 2 && !wait1(&bars[FREE + k], (uint32_t)((c >> 1) - 1) & 1, abort)) break;
+                const int k = c % LY::ST, row = row0 + (chunks - 1 - c) * Q;
+                if (c >= LY::ST && !wait1(&bars[FREE + k], (uint32_t)(c / LY::ST - 1) & 1, abort)) break;
                 tc::mbar_arrive_expect_tx(&bars[X_FULL + k], 4 * XQ);
                 for (int q = 0; q < 4; ++q)
                     for (int j = 0; j < R / 64; ++j)
@@ -967,8 +991,8 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                     tc::tma_load_2d(sm + LY::b(k) + j * PANEL, &map_b, rw.g * DK + 64 * j, row, &bars[B_FULL + k]);
                 ++issued;
             }
-            for (int k = 0; k < 2; ++k) {
-                const int m = (issued + 1 - k) / 2;
+            for (int k = 0; k < LY::ST; ++k) {
+                const int m = (issued + LY::ST - 1 - k) / LY::ST;
                 if (m) {
                     drain(&bars[B_FULL + k], (m - 1) & 1);
                     drain(&bars[X_FULL + k], (m - 1) & 1);
@@ -976,7 +1000,7 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             }
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ------------------------------------------------ products
         {
             const uint32_t lead = tc::elect_one() ? 1u : 0u;
@@ -985,9 +1009,9 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
             constexpr uint64_t ROWS = 16 * 128 / 16;
             bool ok = true;
             for (int c = 0; ok && c < n_chunks; ++c) {
-                const uint32_t par = c & 1;
-                const uint64_t bd = tc::smem_desc(tc::smem_u32(sm + LY::b(par)), PANEL, 1024, tc::SWZ_128);
-                if (!(ok = wait_warp(&bars[B_FULL + par], (c >> 1) & 1, abort))) break;
+                const uint32_t par = c & 1, k = c % LY::ST;
+                const uint64_t bd = tc::smem_desc(tc::smem_u32(sm + LY::b(k)), PANEL, 1024, tc::SWZ_128);
+                if (!(ok = wait_warp(&bars[B_FULL + k], (uint32_t)(c / LY::ST) & 1, abort))) break;
 #pragma unroll 1
                 for (int g = 0; g < 8; ++g) {
                     if (!(ok = wait_warp(&bars[W_FULL + g], par, abort))) break;
@@ -997,15 +1021,15 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                         tc::mma_ts_f16_by(lead, tb + T_S, tb + T_W8 + W_PLACE * g + 8 * i, bd + g * ROWS, ID_S, c + g + i > 0);
                     tc::mma_commit_by(lead, &bars[W_FREE + g]);
                 }
-                if (ok) tc::mma_commit_by(lead, &bars[FREE + par]);  // (W of the chunk has been made, so x has been read too)
+                if (ok) tc::mma_commit_by(lead, &bars[FREE + k]);  // (W of the chunk has been made, so x has been read too)
             }
             tc::mma_commit_by(lead, &bars[DONE]);
             if (!ok) drain(&bars[DONE], 0);
         }
         __syncwarp();
-    } else if (warp - 10 < NH) {
+    } else if (warp - 18 < NH) {
         // ------------------------------------------------ weights of head h, from the last chunk
-        const int h = warp - 10;
+        const int h = warp - 18;
         const bool live = h == 0 || rw.two;
         const float A = live ? in.A[rw.h0 + h] : 0.f, bias = live && in.dt_bias ? in.dt_bias[rw.h0 + h] : 0.f;
         const int m = live ? Q : 0;
@@ -1025,7 +1049,7 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         if (ok && live && rw.r0 == 0 && lane == 0) a.seg_decay[out * p.H + rw.h0 + h] = behind;
     }
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tb, T_COLS);
     }

@@ -66,12 +66,13 @@ struct Layout {
     DL_HD static constexpr int scal(int i, int h) { return SCAL + (i * NH + h) * SCAL_BYTES; }
 };
 
-// The kernel of segments' end states: b and x in two buffers, a chunk's weights.
+// The kernel of segments' end states: three chunks of b and x, two of weights.
 template <int DK, int NH>
 struct EndLayout {
     static constexpr int KP = DK / 64, CTILE = KP * PANEL;
-    static constexpr int B = 0, X = 2 * CTILE, SCAL = X + 2 * 4 * XQ, SCAL_BYTES = Q * 4;
-    static constexpr int BAR = SCAL + 2 * NH * SCAL_BYTES, N_BAR = 27;
+    static constexpr int ST = 3;  // chunks of b and x in flight
+    static constexpr int B = 0, X = ST * CTILE, SCAL = X + ST * 4 * XQ, SCAL_BYTES = Q * 4;
+    static constexpr int BAR = SCAL + 2 * NH * SCAL_BYTES, N_BAR = 30;
     static constexpr int TSLOT = BAR + 8 * N_BAR, ABORT = TSLOT + 4, BYTES = ABORT + 12;
     static constexpr int REQUEST = BYTES + 1024;
     static_assert(REQUEST <= SMEM_LIMIT, "shared memory of a block");
