@@ -171,8 +171,20 @@ struct SsmParams {
 cudaError_t launch_ssm_prompt(const SsmParams &p, const SeqIdx &q, void *work, cudaStream_t st);
 cudaError_t launch_ssm_step(const SsmParams &p, const SeqIdx &q, cudaStream_t st);
 // The prompts' scan on the tcgen05 tensor cores (ssm_tc.cu), for bfloat16 inputs.
+// `g`: segments of g.len tokens; `split`: sequences may have several.
+struct SsmSegs {
+    int len;
+    // sequences of several segments, [segments, H, d_v, d_k] and [segments, H]: a
+    // segment's own end state and log decay, then the state in front of it
+    float *state = nullptr, *decay = nullptr;
+};
+constexpr int SMS = 148;  // of a B200: the workspace's size must not depend on the device
+// Segment length of a call, or 0 (not split).
+inline int ssm_seg_len(int T, int n_seq, int H, int dv) { return seg_len_for(T, n_seq, ((long long)H * dv + 127) / 128, 128, SMS); }
 bool ssm_tc_supported(const SsmParams &p);
-cudaError_t launch_ssm_tc(const SsmParams &p, const SeqIdx &q, void *work, cudaStream_t st);
+cudaError_t launch_ssm_tc(const SsmParams &p, const SeqIdx &q, const SsmSegs &g, bool split, cudaStream_t st);
+// End states -> the states in front of the segments, in place (ssm_tc.cu).
+cudaError_t launch_ssm_join(const SsmParams &p, const SeqIdx &q, const SsmSegs &g, cudaStream_t st);
 cudaError_t read_ssm_faults(unsigned int *out, bool clear);
 size_t ssm_work_bytes(int T, int n_seq, int H, int dk, int dv);
 

@@ -294,8 +294,14 @@ cudaError_t launch_typed(const NormParams &p, cudaStream_t st) {
         if (p.width <= 16384) return go(rms_norm_kernel<XT, RT, RES, WT, 8, 2>, (p.width / 8 + 1) / 2);
         return go(rms_norm_kernel<XT, RT, RES, WT, 8, 4>, (p.width / 8 + 3) / 4);
     }
+    // Single columns: a warp on one group as long as that gives a block, then on as
+    // few as fit (1021 rows of 2501 bfloat16 columns to 8 bits: 9.8 us with one, 11.0
+    // with two, 16.0 with four; 500 of 5001: 8.7 us with two, 11.0 with four; 300 of
+    // 15999: 19.7 us with four, 46 with eight, which no longer fit the registers).
     const int groups = (p.width + 127) / 128;
+    if (groups <= 32) return go(rms_norm_kernel<XT, RT, RES, WT, 1, 4>, groups * 32);
     if (groups <= 64) return go(rms_norm_kernel<XT, RT, RES, WT, 1, 8>, (groups + 1) / 2 * 32);
+    if (groups <= 128) return go(rms_norm_kernel<XT, RT, RES, WT, 1, 16>, (groups + 3) / 4 * 32);
     return go(rms_norm_kernel<XT, RT, RES, WT, 1, 32>, (groups + 7) / 8 * 32);
 }
 

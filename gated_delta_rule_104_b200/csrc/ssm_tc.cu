@@ -34,7 +34,11 @@
 // Each product's time at d_k = 128 is 512 cycles of the tensor pipe, W^T B three
 // times that: 3072 a chunk. What the other warps issue is as much, so their loops
 // are short (unrolled over a tile they waited for instructions five cycles for
-// each one issued: 320 us where the loops take 234 us, before other changes).
+// each one issued: 320 us where the loops took 234 us, before other changes).
+// A chunk takes 5300 cycles, bound by the chain from G over P to P X with y's
+// epilogue behind it and by the issue slots (6500 with a gate): 24 ragged prompts
+// of 16263 tokens on 32 heads of 128 x 128 take 153 us, where moving their bytes
+// takes 47.
 //
 // What is not a number stays where the recurrence has it: products would
 // spread it, as a weight of zero times NaN is NaN. Rows behind the segment are
@@ -56,7 +60,6 @@ namespace {
 
 using namespace stc;
 
-constexpr int SMS = 148;  // of a B200: the workspace's size must not depend on the device
 
 struct Args {
     SsmParams p;
@@ -217,7 +220,7 @@ __device__ __forceinline__ void store_row16(bf16 *p, const uint32_t (&v)[16]) {
 // Tile k of at most 32 sequences taken from the longest to the shortest (by a
 // whole warp): its sequence, or -1, and the segment in it. Blocks start in this
 // order, so the short ones fill in behind the long ones. (Prompts of 17 to 5000
-// tokens on 32 heads: BY_LENGTH us; 182 in the sequences' own order.)
+// tokens on 32 heads: 153 us; 182 in the sequences' own order.)
 __device__ __forceinline__ int tile_by_length(const SeqIdx &q, int k, int len, int lane, int &seg) {
     int s0, n = -1, first = 0;
     if (lane < q.n_seq) seq_range(q, lane, s0, n);
@@ -1058,23 +1061,22 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
 // Segments' own end states -> the states in front of them, in place: a thread
 // takes four elements of one sequence's state through its segments.
 template <class ST>
-__global__ void __launch_bounds__(256) ssm_join_kernel(const Args a, long long quads_per_seq) {
+__global__ void __launch_bounds__(256) ssm_join_kernel(const SsmParams p, const SeqIdx q, const SsmSegs g, long long quads_per_seq) {
     const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
     int seg = 0, s0, n;
-    const int i = seq_of_tile(a.q, (int)blockIdx.y, a.seg_len, seg, 0);
+    const int i = seq_of_tile(q, (int)blockIdx.y, g.len, seg, 0);
     if (i < 0 || seg != 0 || id >= quads_per_seq) return;
-    const int slot = seq_slot(a.q, i);
-    if (!seq_range(a.q, i, s0, n) || slot < 0) return;
-    const int segs = segs_of(n, a.seg_len);
+    const int slot = seq_slot(q, i);
+    if (!seq_range(q, i, s0, n) || slot < 0) return;
+    const int segs = segs_of(n, g.len);
     if (segs < 2) return;
-    const SsmParams &p = a.p;
     const long long at = id * 4, per = quads_per_seq * 4;
     const int h = (int)(at / ((long long)p.dv * p.dk));
-    const long long base = seg_base(s0, a.seg_len);
+    const long long base = seg_base(s0, g.len);
     float s[4];
     load_vec<4>(static_cast<const ST *>(p.S) + slot * per + at, s);
-    float4 *e = reinterpret_cast<float4 *>(a.seg_state + base * per + at);
-    const float *dec = a.seg_decay + base * p.H + h;
+    float4 *e = reinterpret_cast<float4 *>(g.state + base * per + at);
+    const float *dec = g.decay + base * p.H + h;
     constexpr int AHEAD = 6;  // segments whose loads are in flight
     for (int j0 = 0; j0 < segs; j0 += AHEAD) {
         float4 own[AHEAD];
@@ -1115,13 +1117,8 @@ cudaError_t row_map(CUtensorMap *m, const void *base, long long cols, long long 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Segment length of a call, or 0 (not split).
-int ssm_seg_len(int T, int n_seq, int H, int dv) {
-    return seg_len_for(T, n_seq, ((long long)H * dv + R - 1) / R, Q, SMS);
-}
-
 template <class ST, int DK, int NH, bool GATE>
-cudaError_t launch_typed(const SsmParams &p, const SeqIdx &q, void *work, cudaStream_t st) {
+cudaError_t launch_typed(const SsmParams &p, const SeqIdx &q, const SsmSegs &g, bool split, cudaStream_t st) {
     using LY = Layout<DK, NH, GATE>;
     auto kern = ssm_tc_kernel<ST, DK, NH, GATE>;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), LY::REQUEST);
@@ -1136,23 +1133,15 @@ cudaError_t launch_typed(const SsmParams &p, const SeqIdx &q, void *work, cudaSt
     mz = my;  // (not read without a gate)
     if (GATE && (e = row_map(&mz, in.z, yw, q.T, in.z_stride, 32, 16)) != cudaSuccess) return e;
     const int per = p.H / p.G;
-    const long long state = (long long)p.H * p.dv * DK;  // of a sequence
-    int seg_len = ssm_seg_len(q.T, q.n_seq, p.H, p.dv);
-    float *ws = seg_len ? static_cast<float *>(work) : nullptr;
-    const bool split = seg_len != 0;
-    if (!split) seg_len = (int)std::min<long long>(((long long)q.T + Q - 1) / Q * Q, 0x7fffff80LL);
-    Args a{p, q, seg_len, NH == 2 ? p.G * ((per + 1) / 2) : p.H * (p.dv / R), ws,
-           split ? ws + seg_count(q.T, seg_len) * state : nullptr};
+    Args a{p, q, g.len, NH == 2 ? p.G * ((per + 1) / 2) : p.H * (p.dv / R), g.state, g.decay};
     const long long blocks = ((long long)q.T / a.seg_len + q.n_seq) * a.units;
     if (split) {
         using LE = EndLayout<DK, NH>;
         auto ends = ssm_tc_ends_kernel<DK, NH>;
         if ((e = allow_smem(reinterpret_cast<const void *>(ends), LE::REQUEST)) != cudaSuccess) return e;
-        const unsigned ends_max = (unsigned)(q.T / seg_len);  // segments with another behind them
-        ends<<<ends_max * (unsigned)a.units, END_THREADS, LE::REQUEST, st>>>(mx, mb, a);
+        ends<<<(unsigned)(q.T / g.len) * (unsigned)a.units, END_THREADS, LE::REQUEST, st>>>(mx, mb, a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        ssm_join_kernel<ST><<<dim3((unsigned)((state / 4 + 255) / 256), ends_max), 256, 0, st>>>(a, state / 4);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_ssm_join(p, q, g, st)) != cudaSuccess) return e;
     }
     kern<<<(unsigned)blocks, THREADS, LY::REQUEST, st>>>(mx, mb, mc, my, mz, a);
     return cudaGetLastError();
@@ -1165,14 +1154,24 @@ size_t ssm_work_bytes(int T, int n_seq, int H, int dk, int dv) {
     return len ? (size_t)seg_count(T, len) * H * ((size_t)dv * dk + 1) * sizeof(float) : 0;
 }
 
+cudaError_t launch_ssm_join(const SsmParams &p, const SeqIdx &q, const SsmSegs &g, cudaStream_t st) {
+    const long long quads = (long long)p.H * p.dv * p.dk / 4;
+    const dim3 grid((unsigned)((quads + 255) / 256), (unsigned)(q.T / g.len));
+    if (p.s_dt == DL_BF16)
+        ssm_join_kernel<bf16><<<grid, 256, 0, st>>>(p, q, g, quads);
+    else
+        ssm_join_kernel<float><<<grid, 256, 0, st>>>(p, q, g, quads);
+    return cudaGetLastError();
+}
+
 bool ssm_tc_supported(const SsmParams &p) { return p.in.dtype == DL_BF16 && tc::encoder() != nullptr; }
 
-cudaError_t launch_ssm_tc(const SsmParams &p, const SeqIdx &q, void *work, cudaStream_t st) {
+cudaError_t launch_ssm_tc(const SsmParams &p, const SeqIdx &q, const SsmSegs &g, bool split, cudaStream_t st) {
     auto with_nh = [&](auto s, auto dk) -> cudaError_t {
         using ST = decltype(s);
         constexpr int DK = decltype(dk)::value;
-        if (p.in.z) return p.dv == 64 ? launch_typed<ST, DK, 2, true>(p, q, work, st) : launch_typed<ST, DK, 1, true>(p, q, work, st);
-        return p.dv == 64 ? launch_typed<ST, DK, 2, false>(p, q, work, st) : launch_typed<ST, DK, 1, false>(p, q, work, st);
+        if (p.in.z) return p.dv == 64 ? launch_typed<ST, DK, 2, true>(p, q, g, split, st) : launch_typed<ST, DK, 1, true>(p, q, g, split, st);
+        return p.dv == 64 ? launch_typed<ST, DK, 2, false>(p, q, g, split, st) : launch_typed<ST, DK, 1, false>(p, q, g, split, st);
     };
     auto with_dk = [&](auto s) -> cudaError_t {
         return p.dk == 64 ? with_nh(s, std::integral_constant<int, 64>{}) : with_nh(s, std::integral_constant<int, 128>{});
