@@ -439,7 +439,7 @@ static dl_status seq_checks(const int *seq_start, bool ragged, int n_seq, int T,
     if (n_seq < 1) return fail(DL_ERR_INVALID_ARG, "the number of sequences (%d) must be >= 1", n_seq);
     if (P < n_seq) return fail(DL_ERR_INVALID_ARG, "%d sequences need distinct slots but P=%d", n_seq, P);
     if (T < 0) return fail(DL_ERR_INVALID_ARG, "T=%d is negative", T);
-    b[0] = {"seq_start", seq_start, (size_t)(n_seq + 1) * sizeof(int), 4, !ragged};
+    b[0] = {"seq_start", seq_start, ((size_t)n_seq + 1) * sizeof(int), 4, !ragged};
     b[1] = {"slot", slot, (size_t)n_seq * sizeof(int), 4, slot == nullptr};
     b[2] = {"status", status, sizeof(int), 4, status == nullptr};
     return DL_OK;

@@ -567,3 +567,192 @@ def test_a_layer_direct_on_another_stream_and_replayed(g, prompt, dtype):
         for k in names:
             assert torch.equal(cap[k], want[k]), (turn, k)
     del graph
+
+
+# ------------------------------------------------------------------ many rows, far rows
+
+@pytest.mark.parametrize("out", [BF16, torch.int8])
+@pytest.mark.parametrize("width", [4097, 5001, 8191, 16383])
+def test_norm_of_odd_widths(g, width, out):
+    """Rows that no 16-byte access fits, by every number of columns a thread holds."""
+    rng = gen(width)
+    x, r, w = randn(rng, 3, width).to(BF16), randn(rng, 3, width), 1 + 0.1 * randn(rng, width)
+    y = torch.zeros(3, width, dtype=out, device="cuda")
+    h = torch.empty_like(r)
+    scale = torch.zeros(3, -(-width // 128), device="cuda") if out == torch.int8 else None
+    g.dl_rms_norm(x, w, 1e-5, y, residual=r, residual_out=h, scale=scale, group=128 if scale is not None else 0)
+    want_h, want = R.norm(x, r, w, 1e-5)
+    R.assert_within(h, want_h, R.U32 * want_h.abs(), "residual")
+    if scale is None:
+        R.assert_within(y, want, (32 * R.U32 + 2.0 ** -8) * want.abs(), "y")
+    else:
+        got = y.float() * scale.repeat_interleave(128, 1)[:, :width]
+        step = torch.nn.functional.pad(want, (0, -width % 128)).view(3, -1, 128).abs().amax(2) / 127
+        R.assert_within(scale, step, 2.0 ** -18 * step, "scale")
+        step = step.repeat_interleave(128, 1)[:, :width]
+        R.assert_within(got, want, 0.5 * step * (1 + 2.0 ** -12) + 2.0 ** -12 * step, "values")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("channels,tokens", [(301, 9000), (1024, 22000)])
+def test_conv_prompt_that_fills_the_gpu(g, channels, tokens, dtype):
+    """Long tiles of tokens: a few long sequences among many short and empty ones."""
+    rng = gen(channels)
+    lens = [tokens // 2, 0, 1, 31, 32, 33, tokens // 2 - 300] + [k % 4 for k in range(60)]
+    s, seq = starts(lens)
+    T = s[-1] + 5
+    x, w = randn(rng, T, channels).to(dtype), randn(rng, channels, 4).to(dtype)
+    bias = randn(rng, channels).to(dtype)
+    state = randn(rng, len(lens), 3, channels).to(dtype)
+    old, y = state.clone(), torch.full((T, channels), 7.0, dtype=dtype, device="cuda")
+    g.dl_conv_prompt(x, w, bias, state, seq, None, y)
+    for i, n in enumerate(lens):
+        line = torch.cat([old[i], x[s[i]:s[i + 1]]])
+        assert torch.equal(state[i], line[n:])
+        want, mag = R.conv(line, w, bias)
+        bound = 1.1 * 6 * R.U32 * mag + (FAST[dtype] * R.U32 + R.half_step(dtype)) * want.abs() + 1e-38
+        R.assert_within(y[s[i]:s[i + 1]], want, bound, f"sequence {i}")
+    assert bool((y[s[-1]:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,G,dk,dv", [(5, 1, 128, 64), (6, 2, 64, 64), (3, 3, 64, 128)])
+@pytest.mark.parametrize("longest", [6, 90])
+def test_ssm_prompt_of_many_sequences(g, longest, H, G, dk, dv, dtype):
+    """More sequences than are ordered by length, in few tokens each and in many."""
+    lens = [(7 * k) % (longest + 1) for k in range(70)]
+    check_prompt(g, lens, H, G, dk, dv, dtype, F32, gate=G == 2, seed=H, first=1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", [False, True])
+def test_ssm_prompt_keeps_what_is_no_number_across_segments(g, dtype, gate):
+    """As above, in a sequence whose segments run side by side: one channel's NaN in
+    an early segment reaches that channel's later tokens and nothing else."""
+    rng = gen(16)
+    H, dk, dv, n = 1, 64, 64, 4000
+    assert g.dl_ssm_work_bytes(n, 1, H, dk, dv) > 0
+    m = scan_inputs(rng, n, H, 1, dk, dv, dtype, gate, 0.02)
+    S0 = 0.5 * randn(rng, 1, H, dv, dk)
+    _, seq = starts([n])
+
+    def run(m):
+        S, y = S0.clone(), torch.zeros(n, H, dv, dtype=dtype, device="cuda")
+        run_prompt(g, S, seq, None, m, y)
+        return S, y
+
+    S, y = run(m)
+    m["x"][700, 0, 5] = float("nan")
+    S2, y2 = run(m)
+    keep = [e for e in range(dv) if e != 5]
+    assert torch.equal(y2[:, :, keep], y[:, :, keep]) and torch.equal(S2[:, :, keep], S[:, :, keep])
+    assert torch.equal(y2[:700], y[:700]) and bool(y2[700:, 0, 5].isnan().all()) and bool(S2[0, 0, 5].isnan().all())
+
+
+@pytest.fixture(scope="module")
+def far():
+    """2.2e9 bfloat16 elements: rows and slots whose offsets pass 32 bits."""
+    buf = torch.empty(2_200_000_000, dtype=BF16, device="cuda")
+    yield buf
+    del buf
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 9, 200])
+def test_ssm_slots_behind_32_bits(g, far, n, dtype):
+    """The last slots of a large pool, by a prompt (n > 1: token by token, on the
+    tensor cores) and by a step."""
+    rng = gen(17)
+    H, dk, dv = 4, 128, 128
+    per = H * dk * dv
+    P = far.numel() // per
+    assert (P - 2) * per > 2 ** 31
+    pool = far[:P * per].view(P, H, dv, dk)
+    slot = torch.tensor([P - 1, P - 2], dtype=torch.int32, device="cuda")
+    pool[P - 2:] = 0.5 * randn(rng, 2, H, dv, dk).to(BF16)
+    old = pool[P - 2:].clone()
+    wrapped = [((P - 1 - k) * per - 2 ** 31) // per for k in range(2)] + [((P - 1) * per - 2 ** 31) // per + 1]
+    pool[wrapped] = 3.0
+    m = scan_inputs(rng, 2 * n, H, 1, dk, dv, dtype, False)
+    y = torch.zeros(2 * n, H, dv, dtype=dtype, device="cuda")
+    if n == 1:
+        g.dl_ssm_step(pool, slot, m["x"], m["dt"], m["A"], m["b"], m["c"], y, D=m["D"], dt_bias=m["dt_bias"])
+    else:
+        run_prompt(g, pool, torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda"), slot, m, y)
+    for i in range(2):
+        rows = slice(i * n, (i + 1) * n)
+        r = R.scan(old[1 - i], **at(m, rows))
+        by, bS = scan_bounds(r, dtype, BF16, dk, dtype == BF16 and n > 1)
+        R.assert_within(y[rows], r["y"], by, "y")
+        R.assert_within(pool[P - 1 - i], r["S"], bS, "state")
+    assert bool((pool[wrapped] == 3).all())
+
+
+def test_norm_conv_and_scan_of_rows_behind_32_bits(g, far):
+    """Row strides that put the later rows behind 2^31 elements, and a pool of
+    histories as large."""
+    rng = gen(18)
+    rows, width = 260, 128
+    stride = far.numel() // rows // 8 * 8
+    assert (rows - 4) * stride > 2 ** 31
+    x = torch.as_strided(far, (rows, width), (stride, 1))
+    x.copy_(randn(rng, rows, width))
+    near = x.clone()
+    w = 1 + 0.1 * randn(rng, width)
+    a, b = (torch.zeros(rows, width, device="cuda") for _ in range(2))
+    g.dl_rms_norm(x, w, 1e-5, a)
+    g.dl_rms_norm(near, w, 1e-5, b)
+    assert torch.equal(a, b) and bool((b != 0).any())
+    f = randn(rng, width, 4).to(BF16)
+    _, seq = starts([200, 60])
+    st = [torch.zeros(2, 3, width, dtype=BF16, device="cuda") for _ in range(2)]
+    y = [torch.zeros(rows, width, dtype=BF16, device="cuda") for _ in range(2)]
+    for v, s, o in zip((x, near), st, y):
+        g.dl_conv_prompt(v, f, None, s, seq, None, o)
+    assert torch.equal(y[0], y[1]) and torch.equal(st[0], st[1])
+    m = scan_inputs(rng, rows, 2, 1, 64, 64, BF16, True)
+    out = []
+    for v in (x, near):
+        m["x"] = v.view(rows, 2, 64)
+        out.append((torch.zeros(2, 2, 64, 64, device="cuda"), torch.zeros(rows, 2, 64, dtype=BF16, device="cuda")))
+        run_prompt(g, out[-1][0], seq, None, m, out[-1][1])
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    P = far.numel() // (3 * width)
+    pool = far[:P * 3 * width].view(P, 3, width)
+    slot = torch.tensor([P - 1, P - 2], dtype=torch.int32, device="cuda")
+    pool[P - 2:] = st[0].flip(0)
+    o = [torch.zeros(2, width, dtype=BF16, device="cuda") for _ in range(2)]
+    g.dl_conv_step(near[:2], f, None, pool, slot, o[0])
+    g.dl_conv_step(near[:2], f, None, st[0], None, o[1])
+    assert torch.equal(o[0], o[1]) and torch.equal(pool[P - 2:].flip(0), st[0])
+
+
+def test_layer_graphs_that_share_a_workspace(g):
+    """Two captured scans that share their workspace, replayed in turn on one stream."""
+    rng = gen(19)
+    H, dk, dv, n = 2, 64, 64, 3000
+    _, seq = starts([n])
+    work = torch.empty(g.dl_ssm_work_bytes(n, 1, H, dk, dv), dtype=torch.uint8, device="cuda")
+    assert work.numel() > 0
+    calls, graphs = [], []
+    for k in range(2):
+        m = scan_inputs(rng, n, H, 1, dk, dv, BF16, False, 0.02)
+        calls.append((m, torch.zeros(1, H, dv, dk, device="cuda"), torch.zeros(n, H, dv, dtype=BF16, device="cuda")))
+    go = lambda m, S, y: g.dl_ssm_prompt(S, seq, None, m["x"], m["dt"], m["A"], m["b"], m["c"], y, work=work)  # noqa: E731
+    for c in calls:
+        go(*c)
+    want = [(S.clone(), y.clone()) for _, S, y in calls]
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graphs[-1]):
+            go(*c)
+    for _, S, y in calls:
+        S.zero_(), y.zero_()
+    for gr in graphs:
+        gr.replay()
+    torch.cuda.synchronize()
+    for (_, S, y), (S0, y0) in zip(calls, want):
+        assert torch.equal(S, S0) and torch.equal(y, y0)
+    graphs.clear()
