@@ -12,7 +12,6 @@ namespace dl {
 
 namespace {
 
-
 // dt and exp(dt A) of (row, head).
 template <class IT>
 __device__ __forceinline__ void step_size(const dl_ssm &in, long long row, int h, float &dt, float &da) {
@@ -23,11 +22,14 @@ __device__ __forceinline__ void step_size(const dl_ssm &in, long long row, int h
 constexpr int STEP_R = 8;  // state loads a lane has in flight
 
 // One token per sequence. HBM-bound on the state like the eager step, and laid
-// out as that is: a state row over a group of lanes, 16 bytes each, R = 4 rows'
+// out as that is: a state row over a group of lanes, 16 bytes each, R rows'
 // loads in flight per lane before any arithmetic, a shuffle sum per row, no
-// shared memory.
+// shared memory. A lane holds x, z and y of one of the unit's rows, which keeps a
+// float32 state's kernel within the 64 registers of four blocks an SM (256
+// sequences of 32 heads of 128 x 128: 157 us; 187 with each row's x loaded by its
+// lanes and three blocks, 177 with four rows' loads in flight).
 template <class ST, class IT, int DK>
-__global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p, const SeqIdx q, long long num_units) {
+__global__ void __launch_bounds__(256, sizeof(ST) == 4 ? 4 : 3) ssm_step_kernel(const SsmParams p, const SeqIdx q, long long num_units) {
     constexpr int VEC = StateVec<ST>::N, G = DK / VEC, RPW = 32 / G, R = STEP_R, UNIT = R * RPW;
     const long long gid = (long long)blockIdx.x * 256 + threadIdx.x;
     if (gid < q.n_seq) seq_check(q, (int)gid);
@@ -48,33 +50,32 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmParams p, const 
 
     const dl_ssm &in = p.in;
     const int g = h / (p.H / p.G);
-    float bb[VEC], cc[VEC], xr[R], dt, da;
+    float bb[VEC], cc[VEC], xl = 0.f, zl = 0.f, yl = 0.f, dt, da;
     load_vec<VEC>(static_cast<const IT *>(in.b) + b * in.b_stride + g * DK + col, bb);
     load_vec<VEC>(static_cast<const IT *>(in.c) + b * in.c_stride + g * DK + col, cc);
-    const IT *x = static_cast<const IT *>(in.x) + b * in.x_stride + (long long)h * p.dv + r0 + sub;
-#pragma unroll
-    for (int r = 0; r < R; ++r) xr[r] = to_f(x[r * RPW]);
+    // x, z and y of the unit's row `lane`
+    const bool own = lane < UNIT;
+    const long long at = (long long)h * p.dv + r0 + lane;
+    if (own) xl = to_f(static_cast<const IT *>(in.x)[b * in.x_stride + at]);
+    if (own && in.z) zl = to_f(static_cast<const IT *>(in.z)[b * in.z_stride + at]);
     step_size<IT>(in, b, h, dt, da);
-    const float D = in.D ? in.D[h] : 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         float s[VEC], y = 0.f;
         StateVec<ST>::unpack(raw[r], s);
-        const float dx = dt * xr[r];
+        const float dx = dt * __shfl_sync(0xffffffffu, xl, r * RPW + sub);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             s[e] = fmaf(s[e], da, dx * bb[e]);
             y = fmaf(s[e], cc[e], y);
         }
-        y = group_sum<G>(y);
         st_stream(srow + (long long)r * RPW * DK, StateVec<ST>::pack(s));
-        if (lane % G == 0) {
-            const int row = r0 + r * RPW + sub;
-            y = fmaf(D, xr[r], y);
-            if (in.z) y *= silu_f<IT>(to_f(static_cast<const IT *>(in.z)[b * in.z_stride + (long long)h * p.dv + row]));
-            store_f(static_cast<IT *>(p.y) + (b * p.H + h) * p.dv + row, y);
-        }
+        y = __shfl_sync(0xffffffffu, group_sum<G>(y), (lane % RPW) * G);
+        if (lane / RPW == r) yl = y;
     }
+    if (in.D) yl = fmaf(in.D[h], xl, yl);
+    if (in.z) yl *= silu_f<IT>(zl);
+    if (own) store_f(static_cast<IT *>(p.y) + b * p.H * p.dv + at, yl);
 }
 
 // Prompts, token by token: a block keeps ROWS rows of one head's state in
