@@ -468,8 +468,7 @@ int dl_abi_version(void);
 /* Fault word of the library's kernels on the current device. The kernels that
  * wait on on-chip barriers (the tcgen05 merge of dl_log_merge and
  * dl_log_merge_read, the one-kernel form of dl_log_append_read, and the
- * tcgen05 scan of dl_ssm_prompt) bound
- * every such wait; a wait that runs out (about two
+ * tcgen05 scan of dl_ssm_prompt) bound every such wait; a wait that runs out (about two
  * seconds; it means a bug, not a slow GPU) sets bit 0 here, abandons its work
  * (the state it was merging is then unspecified) and returns, so the device
  * stays usable. In the index-guard build (dl_index_guard_build() == 1), bit 1
@@ -482,8 +481,8 @@ int dl_abi_version(void);
 dl_status dl_device_faults(unsigned int *flags, int clear);
 
 /* 1 in the index-guard debug build (libdeltalog_guard.so, compiled with
- * DL_INDEX_GUARD: every shared-memory write of the kernels checks its bounds
- * and alignment first, and a write that fails is skipped and reported through
+ * DL_INDEX_GUARD: every shared-memory write of the log's read and merge
+ * kernels checks its bounds and alignment first, and a write that fails is skipped and reported through
  * dl_device_faults), else 0. The guard build computes the same results as the
  * ordinary one, more slowly. No counterpart on the pages. */
 int dl_index_guard_build(void);
