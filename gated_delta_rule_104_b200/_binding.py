@@ -463,35 +463,44 @@ def dl_pool_flush(pool: Pool, slot, stream=None) -> None:
 # (These calls take a dozen tensors and a kernel of a few microseconds: what is
 # checked of a tensor is checked in one function, by the cheapest queries.)
 
-_codes = None
+_codes = _getdevice = _getstream = _i32 = None
+
+
+def _queries() -> None:
+    """The device, the stream and the dtypes of torch, looked up once."""
+    global _codes, _getdevice, _getstream, _i32
+    torch = _torch()
+    _getdevice, _getstream, _i32 = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, torch.int32
+    _codes = {torch.float32: DL_F32, torch.bfloat16: DL_BF16, torch.int8: DL_I8, torch.float8_e4m3fn: DL_E4M3}
 
 
 def _code_of(t) -> int:
     """dl_dtype of a tensor (as _dtype_code, 8-bit types too)."""
-    global _codes
     if _codes is None:
-        torch = _torch()
-        _codes = {torch.float32: DL_F32, torch.bfloat16: DL_BF16, torch.int8: DL_I8, torch.float8_e4m3fn: DL_E4M3}
-    try:
-        return _codes[t.dtype]
-    except KeyError:
-        raise TypeError(f"unsupported dtype {t.dtype}") from None
+        _queries()
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _float_code(*ts) -> int:
     """The one dl_dtype, float32 or bfloat16, of the tensors that are not None."""
-    code = _code_of(ts[0])
+    dtype = ts[0].dtype
     for t in ts:
-        if t is not None and t.dtype != ts[0].dtype:
+        if t is not None and t.dtype is not dtype:
             raise TypeError("these operands must share one dtype: " + ", ".join(str(u.dtype) for u in ts if u is not None))
+    code = _code_of(ts[0])
     if code > DL_BF16:
-        raise TypeError(f"unsupported dtype {ts[0].dtype} (float32 or bfloat16)")
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
     return code
 
 
 def _device() -> int:
     """The current device: a call launches there, and every operand must lie on it."""
-    return _torch()._C._cuda_getDevice()
+    if _getdevice is None:
+        _queries()
+    return _getdevice()
 
 
 def _misplaced(t, name: str, dev: int):
@@ -501,51 +510,51 @@ def _misplaced(t, name: str, dev: int):
 
 
 def _raw_stream(stream, dev: int) -> int:
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
+    return _getstream(dev) if stream is None else _stream(stream)
 
 
 def _full(t, name: str, shape, dev: int) -> int:
     """Pointer of a contiguous tensor of the given shape on the current device."""
+    if t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.get_device() != dev:
         raise _misplaced(t, name, dev)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _f32(t, name: str, shape, dev: int) -> Optional[int]:
     """The same of a float32 tensor, or None."""
     if t is None:
         return None
-    if _code_of(t) != DL_F32:
+    if _codes.get(t.dtype) != DL_F32:
         raise TypeError(f"{name} must be float32, got {t.dtype}")
     return _full(t, name, shape, dev)
 
 
-def _rows(t, name: str, shape, dev: int):
-    """Pointer and row stride of a tensor whose rows (all dimensions but the first) are contiguous."""
+def _rows(t, name: str, shape, dev: int, width: int):
+    """Pointer and row stride of a tensor whose rows (all dimensions but the first, of `width` elements) are contiguous."""
     if t.get_device() != dev:
         raise _misplaced(t, name, dev)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    width = 1
+    if t.is_contiguous():
+        return t.data_ptr(), width or 1
+    inner = 1
     strides = t.stride()
     for k in range(len(shape) - 1, 0, -1):
-        if shape[k] != 1 and strides[k] != width:
+        if shape[k] != 1 and strides[k] != inner:
             raise ValueError(f"the rows of {name} must be contiguous")
-        width *= shape[k]
-    return t.data_ptr(), strides[0] if shape[0] > 1 else max(width, 1)
+        inner *= shape[k]
+    return t.data_ptr(), strides[0] if shape[0] > 1 else width or 1
 
 
 def _index(t, name: str, n: int, dev: int) -> Optional[int]:
     """Pointer of an int32 tensor of n elements, or None."""
     if t is None:
         return None
-    if t.dtype != _torch().int32:
+    if t.dtype is not _i32:
         raise TypeError(f"{name} must be int32, got {t.dtype}")
     return _full(t, name, (n,), dev)
 
@@ -561,7 +570,7 @@ def dl_rms_norm(x, weight, eps: float, y, residual=None, residual_out=None, scal
         raise ValueError("x must be [rows, width]")
     dev = _device() if x.is_cuda else -2
     rows, width = shape = x.shape
-    xp, xs = _rows(x, "x", shape, dev)
+    xp, xs = _rows(x, "x", shape, dev, width)
     xc, yc = _float_code(x), _code_of(y)
     if (residual is None) != (residual_out is None):
         raise ValueError("residual and residual_out go together")
@@ -603,12 +612,12 @@ def dl_rows_from_8bit(codes, scale, out, group: int = 0, stream=None) -> None:
 def _conv(x, w, bias, state, y, silu, dev):
     if x.dim() != 2 or w.dim() != 2 or state.dim() != 3:
         raise ValueError("x must be [rows, channels], w [channels, taps], state [P, taps - 1, channels]")
-    rows, channels = x.shape
+    rows, channels = shape = x.shape
     taps, P = w.shape[1], state.shape[0]
-    xp, xs = _rows(x, "x", x.shape, dev)
+    xp, xs = _rows(x, "x", shape, dev, channels)
     cv = dl_conv(_full(w, "w", (channels, taps), dev), None if bias is None else _full(bias, "bias", (channels,), dev), channels,
                  taps, _float_code(x, w, bias, state, y), 1 if silu else 0)
-    return cv, xp, xs, rows, _full(state, "state", (P, taps - 1, channels), dev), P, _full(y, "y", (rows, channels), dev)
+    return cv, xp, xs, rows, _full(state, "state", (P, taps - 1, channels), dev), P, _full(y, "y", shape, dev)
 
 
 def dl_conv_prompt(x, w, bias, state, seq_start, slot, y, silu: bool = True, status=None, stream=None) -> None:
@@ -638,19 +647,19 @@ def dl_conv_step(x, w, bias, state, slot, y, silu: bool = True, status=None, str
 def _ssm(S, x, dt, A, b, c, y, D, dt_bias, z, dev):
     if x.dim() != 3 or b.dim() != 3 or S.dim() != 4:
         raise ValueError("S must be [P, H, d_v, d_k], x [rows, H, d_v], b and c [rows, G, d_k]")
-    P, H, dv, dk = S.shape
+    P, H, dv, dk = s_shape = S.shape
     rows, G = x.shape[0], b.shape[1]
     wide, keys, heads = (rows, H, dv), (rows, G, dk), (H,)
-    zp, zs = (None, 0) if z is None else _rows(z, "z", wide, dev)
-    xp, xs = _rows(x, "x", wide, dev)
-    tp, ts = _rows(dt, "dt", (rows, H), dev)
-    bp, bs = _rows(b, "b", keys, dev)
-    cp, cs = _rows(c, "c", keys, dev)
+    zp, zs = (None, 0) if z is None else _rows(z, "z", wide, dev, H * dv)
+    xp, xs = _rows(x, "x", wide, dev, H * dv)
+    tp, ts = _rows(dt, "dt", (rows, H), dev, H)
+    bp, bs = _rows(b, "b", keys, dev, G * dk)
+    cp, cs = _rows(c, "c", keys, dev, G * dk)
     if A is None:
         raise ValueError("A is required")
     m = dl_ssm(xp, xs, tp, ts, bp, bs, cp, cs, zp, zs, _f32(A, "A", heads, dev), _f32(D, "D", heads, dev),
                _f32(dt_bias, "dt_bias", heads, dev), _float_code(x, dt, b, c, y, z))
-    return m, P, H, G, dk, dv, rows, _full(y, "y", wide, dev), _full(S, "S", S.shape, dev), _float_code(S)
+    return m, P, H, G, dk, dv, rows, _full(y, "y", wide, dev), _full(S, "S", s_shape, dev), _float_code(S)
 
 
 def dl_ssm_work_bytes(T: int, n_seq: int, H: int, d_k: int, d_v: int) -> int:
