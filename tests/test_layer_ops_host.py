@@ -224,3 +224,16 @@ def test_bad_sequence_bounds_never_leave_the_rows(replay):
         for i, a, z in got + [e[:3] for e in ends]:
             assert 0 <= start[i] <= a < z <= start[i + 1] <= T
         assert all(0 <= e[3] and e[3] + 1 < places for e in ends)
+
+
+def test_layout_of_the_tensor_core_scan(tmp_path):
+    """Shared and tensor memory of every form of the scan, replayed from the kernel's own layout header."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("g++ not available")
+    exe = str(tmp_path / "ssm_tc_replay")
+    csrc = os.path.join(ROOT, "gated_delta_rule_104_b200", "csrc")
+    subprocess.run([gxx, "-std=c++17", "-O2", "-Wall", "-Werror", f"-I{csrc}", "-o", exe,
+                    os.path.join(HERE, "replay", "ssm_tc_replay.cpp")], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert out.returncode == 0, out.stdout
