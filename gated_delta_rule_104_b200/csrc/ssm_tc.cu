@@ -258,7 +258,9 @@ struct Steps {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             dt[j] = 32 * j + lane < m ? softplus_f(raw[j] + bias) : 0.f;
-            l[j] = w[j] = dt[j] * A;
+            // (a step of e^-128 is 0 in fp32 as any stronger one is; kept there, the sums
+            // resolve 2^-10 behind it, less than an output's rounding)
+            l[j] = w[j] = fmaxf(dt[j] * A, -128.f);
         }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1)

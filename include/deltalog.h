@@ -442,7 +442,8 @@ size_t dl_ssm_work_bytes(int T, int n_seq, int H, int d_k, int d_v);
  *        fp32 and rounded once at the sequence's end)
  *   y    [T, H, d_v] in->dtype
  *   work dl_ssm_work_bytes(...) bytes, 16-byte aligned (null if that is 0),
- *        contents irrelevant between calls
+ *        contents irrelevant between calls (calls that may run at the same
+ *        time need one each)
  * T >= 0, n_seq >= 1, G divides H. */
 dl_status dl_ssm_prompt(void *S, dl_dtype s_dtype, int P, const int *slot, int *status,
                         const dl_ssm *in, const int *seq_start, int n_seq, int T,

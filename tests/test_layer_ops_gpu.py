@@ -342,6 +342,19 @@ def test_ssm_prompt_without_decay_and_with_one_that_forgets_all(g, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("at", [0, 3, 40, 127])
+def test_ssm_prompt_behind_a_step_of_a_million(g, at, dtype):
+    """A step whose log decay is -1e6, then steps of -0.01: sums from the chunk's start must not swallow those."""
+    def change(m):
+        m["A"][:] = -2000.0
+        m["dt"][:] = -12.0  # dt = 6e-6
+        m["dt"][at] = 500.0
+        m["dt_bias"] = None
+
+    check_prompt(g, [200], 2, 1, 64, 64, dtype, F32, gate=False, seed=21, change=change)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_ssm_prompt_keeps_what_is_no_number_where_it_belongs(g, dtype, bad):
     """A NaN or infinity in x at one token and channel, b, c or dt at others: the
