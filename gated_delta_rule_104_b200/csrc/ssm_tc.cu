@@ -27,18 +27,18 @@
 //                token row), half of the columns each
 //   warps 4-7    S: to bfloat16 for C S^T and scaled in place for the next
 //                update (thread = value row); then Y's scaling (thread = token)
-//   warps 8-15   W from X, 32 tokens at a time, two sets of four warps in turn
+//   warps 8-15   W from X, 16 tokens at a time, two sets of four warps in turn
 //   warp 20      TMA: x two chunks ahead, b and c one
-//   warp 21      issues the products: G, W^T B by 32 tokens, C S^T between them, P X
+//   warp 21      issues the products: G, W^T B by 16 tokens, C S^T between them, P X
 //   warps 22-23  step sizes and decays of a chunk (one head each), one ahead
 // Each product's time at d_k = 128 is 512 cycles of the tensor pipe, W^T B three
-// times that: 3072 a chunk. What the other warps issue is as much, so their loops
-// are short (unrolled over a tile they waited for instructions five cycles for
-// each one issued: 320 us where the loops took 234 us, before other changes).
-// A chunk takes 5300 cycles, bound by the chain from G over P to P X with y's
-// epilogue behind it and by the issue slots (6500 with a gate): 24 ragged prompts
-// of 16263 tokens on 32 heads of 128 x 128 take 153 us, where moving their bytes
-// takes 47.
+// times that: 3100 a chunk in all. What the other warps issue is as much, so
+// their loops are short (unrolled over a tile they waited for instructions five
+// cycles for each one issued: 320 us where the loops took 234 us, before other
+// changes). A chunk takes 5300 cycles, bound by the chain from G over P to P X
+// with y's epilogue behind it and by the issue slots (11000 with a gate and two
+// heads of 64): 8 ragged prompts of 16263 tokens on 32 heads of 128 x 128 take
+// 153 us, where moving their bytes takes 47.
 //
 // What is not a number stays where the recurrence has it: products would
 // spread it, as a weight of zero times NaN is NaN. Rows behind the segment are
@@ -73,8 +73,8 @@ struct Args {
 
 enum Bar {
     C_FULL, C_FREE, B_FULL, B_FREE = B_FULL + 2, SC_FULL = B_FREE + 2,
-    SC_FREE = SC_FULL + 2, Z_FULL = SC_FREE + 2, W_FULL = Z_FULL + 24, W_FREE = W_FULL + W_PLACES, S_READY = W_FREE + W_PLACES, G_DONE, P_READY, Y2_DONE, YS_READY, Y_DONE, Y_FREE, ST_DONE,
-    DRAIN, X_FULL  // (then x's places' X_FREE)
+    SC_FREE = SC_FULL + 2, Z_FULL = SC_FREE + 2, W_FULL = Z_FULL + 24, W_FREE = W_FULL + W_PLACES,
+    S_READY = W_FREE + W_PLACES, G_DONE, P_READY, Y2_DONE, YS_READY, Y_DONE, Y_FREE, ST_DONE, DRAIN, X_FULL  // (then x's places' X_FREE)
 };
 
 __device__ __forceinline__ uint64_t globaltimer() {
