@@ -824,6 +824,9 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     return true;
                 };
                 if (!(ok = wait_warp(&bars[C_FULL], par, abort) && wait_warp(&bars[B_FULL + par], par2, abort))) break;
+                // the previous chunk's P X has read P, which lies in G's columns: products with
+                // different accumulators are not ordered by their issue (they share one pipe: no time lost)
+                if (!(ok = c == 0 || wait_warp(&bars[Y_DONE], (c - 1) & 1, abort))) break;
                 tc::tc_fence_after();
                 over_columns(tb + T_G, ck, bk + par * NEXT_B, ID_G);
                 tc::mma_commit_by(lead, &bars[G_DONE]);
