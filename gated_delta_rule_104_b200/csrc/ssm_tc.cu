@@ -254,12 +254,12 @@ struct Steps {
     float dt[4], l[4], u[4], w[4], end;
     // `behind`: log decay behind the chunk that the weights take in as well.
     __device__ __forceinline__ void compute(float bias, float A, int lane, int m, float behind) {
-        float before = 0.f;  // log decay in front of the 32 tokens
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             dt[j] = 32 * j + lane < m ? softplus_f(raw[j] + bias) : 0.f;
-            // (a step of e^-128 is 0 in fp32 as any stronger one is; kept there, the sums
-            // resolve 2^-10 behind it, less than an output's rounding)
+            // (a step of e^-128 is 0 in fp32 as any stronger one is; kept there, sums over 32
+            // tokens stay within 4096, and the exponential of a difference of two is off by
+            // at most 2^-10 behind any number of such steps: a quarter of a bf16 rounding)
             l[j] = w[j] = fmaxf(dt[j] * A, -128.f);
         }
 #pragma unroll
@@ -270,13 +270,13 @@ struct Steps {
                 if (lane >= off) l[j] += a;
                 if (lane + off < 32) w[j] += b;
             }
+        end = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            l[j] += before;
-            before = __shfl_sync(0xffffffffu, l[j], 31);
-            u[j] = expf(before - l[j]) * dt[j];
+            const float all = __shfl_sync(0xffffffffu, l[j], 31);
+            u[j] = expf(all - l[j]) * dt[j];
+            end += all;
         }
-        end = before;
 #pragma unroll
         for (int j = 3; j >= 0; --j) {  // behind: of the 32 tokens
             const float own = __shfl_down_sync(0xffffffffu, w[j], 1), all = __shfl_sync(0xffffffffu, w[j], 0);
@@ -291,8 +291,16 @@ struct Steps {
             sc[Scal::L + 32 * j + lane] = l[j] * LOG2E;
             sc[Scal::U + 32 * j + lane] = u[j];
             sc[Scal::W + 32 * j + lane] = w[j];
-            if (lane == 31) sc[Scal::RB + j] = l[j] * LOG2E;
         }
+        // lane 4 i + j: blocks behind j and in front of i; lane 5 i: all in front of i
+        const int i = lane >> 2, j = lane % 4 == i ? -1 : lane & 3;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const float all = __shfl_sync(0xffffffffu, l[k], 31);
+            if (k > j && k < i) sum += all;
+        }
+        if (lane < 16) sc[Scal::RB + lane] = sum * LOG2E;
         if (lane == 31) sc[Scal::E] = expf(end);
     }
 };
@@ -312,7 +320,9 @@ __device__ __noinline__ void add_no_numbers(const SsmParams &p, long long row0, 
         const bf16 *b = static_cast<const bf16 *>(in.b) + (row0 + s) * in.b_stride + (long long)g * p.dk;
         float f = 0.f;
         for (int e = 0; e < p.dk; ++e) f = fmaf(to_f(c[e]), to_f(b[e]), f);
-        f *= exp2f(sc[Scal::L + t] - sc[Scal::L + s]) * sc[Scal::DT + s];
+        float l = sc[Scal::L + t] - sc[Scal::L + s];
+        if ((t ^ s) >> 5) l += sc[Scal::between(t >> 5, s >> 5)] + sc[Scal::L + (s | 31)];  // of different 32 tokens
+        f *= exp2f(l) * sc[Scal::DT + s];
         if (s == t && in.D) f += in.D[h];
         for (int e = 0; e < cols; ++e) {
             const float v = to_f(x[(row0 + s) * in.x_stride + e]);
@@ -453,7 +463,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                     const float *sc = scal(c, h);
                     const float lt = lth[h];
                     if (!diagonal) {
-                        const float v = ex2_ftz(lt - sc[Scal::RB + (k >> 1)]);
+                        const float v = ex2_ftz(lt + sc[Scal::between(quad, k >> 1)]);
                         const uint64_t vv = pair(v, v);
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
@@ -643,7 +653,8 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 
             float ex[NH];
 #pragma unroll
-            for (int k = 0; k < NH; ++k) ex[k] = ex2_ftz(scal(c, k)[Scal::L + r]);
+            for (int k = 0; k < NH; ++k)  // (from r: an index kept in a register of its own spilled others, 161 -> 174 us)
+                ex[k] = ex2_ftz(scal(c, k)[Scal::L + r] + scal(c, k)[Scal::before(r >> 5)]);
             arrive(SC_FREE + par);
             if (!(ok = wait_warp(&bars[Y2_DONE], par, abort))) break;
             tc::tc_fence_after();

@@ -36,11 +36,17 @@ DL_HD inline constexpr int xq_off(int row, int piece) {
 DL_HD inline constexpr int gate_off(int row, int piece) { return row * 32 + ((piece ^ ((row >> 2) & 1)) << 4); }
 
 // Per chunk and head, from the step sizes (floats): the base-2 log decay from
-// the chunk's start through token t, l; u = 2^(l at the end of its 32 tokens - l) dt;
-// dt; w = exp(log decay behind the token, within the chunk) dt; l at the end of
-// each 32 tokens; exp of the whole chunk's log decay.
+// the start of a token's 32 through token t, l; u = 2^(l at the end of its 32 tokens
+// - l) dt; dt; w = exp(log decay behind the token, within the chunk) dt; the base-2
+// log decays between blocks of 32 tokens; exp of the whole chunk's log decay.
+// Sums over 32 tokens only, so that steps which forget all leave the weak steps
+// of other blocks their accuracy.
 struct Scal {
-    static constexpr int L = 0, U = Q, DT = 2 * Q, W = 3 * Q, RB = 4 * Q, E = 4 * Q + 4, FLOATS = 4 * Q + 8;
+    static constexpr int L = 0, U = Q, DT = 2 * Q, W = 3 * Q, RB = 4 * Q, E = RB + 16, FLOATS = RB + 20;
+    // Place of the log decay of the blocks behind block j and in front of block i > j,
+    DL_HD static constexpr int between(int i, int j) { return RB + 4 * i + j; }
+    // and of all blocks of the chunk in front of block i.
+    DL_HD static constexpr int before(int i) { return RB + 5 * i; }
 };
 
 template <int DK, int NH, bool GATE>

@@ -1,0 +1,83 @@
+"""GPU tests of the norm, the short convolution and the selective scan at the
+edges of their contract, beside test_layer_ops_gpu.py. References in 64 bits;
+u = 2^-24 is half a float32 step, relative, and a rounding to bfloat16 is off by
+at most 2^-8 of the value as R.half_step counts it."""
+import pytest
+
+from tests import layer_ref as R
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def g():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import gated_delta_rule_104_b200 as g
+
+    g.load()
+    return g
+
+
+@pytest.fixture(autouse=True)
+def _no_wait_ran_out(g):
+    yield
+    assert g.dl_device_faults(clear=True) == 0
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def starts(lens):
+    s = [0]
+    for n in lens:
+        s.append(s[-1] + n)
+    return torch.tensor(s, dtype=torch.int32, device="cuda")
+
+
+def prompt(g, S, lens, x, dt, A, b, c, **k):
+    """The scan over prompts laid end to end; returns y (S is advanced)."""
+    T, H, dv = x.shape
+    y = torch.full((T, H, dv), 7.0, dtype=x.dtype, device="cuda")
+    work = torch.empty(g.dl_ssm_work_bytes(T, len(lens), H, b.shape[2], dv), dtype=torch.uint8, device="cuda")
+    g.dl_ssm_prompt(S, starts(lens), None, x, dt, A, b, c, y, work=work, **k)
+    return y
+
+
+# ------------------------------------------------------------------ decays of the tensor-core scan
+
+@pytest.mark.parametrize("strong", [16, 40, 100, 112, 120])
+def test_ssm_prompt_decays_behind_many_strong_steps(g, strong):
+    """`strong` steps that forget all, then weak ones in the same chunk.
+
+    One token has x = 1, the state is zero, and c . b is a number g of 8 bits. So y
+    at a later token is the decayed score g exp(l_t - l_s) dt rounded to bfloat16,
+    once, and the score's exponential may be off by 2^-10 (and 32 u by the steps and
+    products): y lies between the roundings of the ends of that interval.
+    """
+    H, d, n = 16, 64, 128
+    rng = gen(strong)
+    dt = (-6 + torch.randn(n, H, generator=rng, device="cuda")).to(BF16)
+    dt[:strong] = 500.0
+    A = -(1 + 15 * torch.rand(H, generator=rng, device="cuda"))
+    b, c = torch.zeros(n, H, d, dtype=BF16, device="cuda"), torch.zeros(n, H, d, dtype=BF16, device="cuda")
+    b[:, :, 0] = 1.0
+    c[:, :, 0] = (1 + torch.randint(128, (n, H), generator=rng, device="cuda") / 128).to(BF16)
+    lost = torch.zeros(n, H, d, dtype=BF16, device="cuda")
+    steps = torch.logaddexp(R.f64(dt), torch.zeros(n, H, dtype=torch.float64))
+    for s in sorted({strong, (strong + 127) // 2, 125}):
+        x = lost.clone()
+        x[s] = 1.0
+        y = prompt(g, torch.zeros(1, H, d, d, device="cuda"), [n], x, dt, A, b, c)
+        decay = (steps * R.f64(A)).cumsum(0)
+        want = R.f64(c[:, :, 0]) * torch.exp(decay - decay[s]) * steps[s]
+        off = 2.0 ** -10 + 32 * R.U32
+        low, high = ((want * f).float().to(BF16).double() for f in (1 - off, 1 + off))
+        got = R.f64(y)[s:]
+        assert bool((got == got[:, :, :1]).all()) and bool((y[:s] == 0).all())
+        outside = (got[:, :, 0] < low[s:]) | (got[:, :, 0] > high[s:])
+        assert not bool(outside.any()), (s, int(outside.sum()), outside.nonzero()[0].tolist())
