@@ -197,9 +197,10 @@ __global__ void __launch_bounds__(4 * ROWS) ssm_scan_kernel(const SsmParams p, c
             if constexpr (!ENDS) cs[bt][bc + e] = rc[e];
         }
         if (tid < SCAN_TOK) {
-            const float dt = t0 + tid < n ? softplus_f(rdt + bias) : 0.f;
-            steps[tid] = make_float2(dt, expf(dt * A));
-            decay += dt * A;
+            const bool in = t0 + tid < n;  // (no decay behind the segment: 0 A is no number for an A of -inf)
+            const float dt = in ? softplus_f(rdt + bias) : 0.f, ld = in ? dt * A : 0.f;
+            steps[tid] = make_float2(dt, expf(ld));
+            decay += ld;
         }
         __syncthreads();
         fetch(t0 + SCAN_TOK);

@@ -256,11 +256,12 @@ struct Steps {
     __device__ __forceinline__ void compute(float bias, float A, int lane, int m, float behind) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            dt[j] = 32 * j + lane < m ? softplus_f(raw[j] + bias) : 0.f;
+            const bool in = 32 * j + lane < m;  // (no decay behind the segment: 0 A is no number for an A of -inf)
+            dt[j] = in ? softplus_f(raw[j] + bias) : 0.f;
             // (a step of e^-128 is 0 in fp32 as any stronger one is; kept there, sums over 32
             // tokens stay within 4096, and the exponential of a difference of two is off by
             // at most 2^-10 behind any number of such steps: a quarter of a bf16 rounding)
-            l[j] = w[j] = fmaxf(dt[j] * A, -128.f);
+            l[j] = w[j] = in ? fmaxf(dt[j] * A, -128.f) : 0.f;
         }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1)

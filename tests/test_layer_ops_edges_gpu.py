@@ -81,3 +81,32 @@ def test_ssm_prompt_decays_behind_many_strong_steps(g, strong):
         assert bool((got == got[:, :, :1]).all()) and bool((y[:s] == 0).all())
         outside = (got[:, :, 0] < low[s:]) | (got[:, :, 0] > high[s:])
         assert not bool(outside.any()), (s, int(outside.sum()), outside.nonzero()[0].tolist())
+
+
+def layer_inputs(seed, n, H, dk, dv, dtype):
+    rng = gen(seed)
+    randn = lambda *s: torch.randn(*s, generator=rng, device="cuda")  # noqa: E731
+    return [randn(n, H, dv).to(dtype), (randn(n, H) - 2).to(dtype), -1 - 8 * torch.rand(H, generator=rng, device="cuda"),
+            randn(n, 1, dk).to(dtype), randn(n, 1, dk).to(dtype)]
+
+
+# a ragged call; few tokens a sequence; one long sequence in segments
+CALLS = [[70, 1, 300], [5, 0, 9], [3000]]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dv", [64, 128])
+@pytest.mark.parametrize("lens", CALLS, ids=str)
+def test_ssm_prompt_of_a_head_that_forgets_at_once(g, lens, dv, dtype):
+    """A of -inf, the strongest decay there is: as any that leaves nothing of the state, to the bit."""
+    H, dk = 3, 64
+    x, dt, A, b, c = layer_inputs(31, sum(lens), H, dk, dv, dtype)
+    out = []
+    for a in (-1e30, float("-inf")):
+        A[1] = a
+        S = torch.ones(len(lens), H, dv, dk, device="cuda")
+        out.append((S, prompt(g, S, lens, x, dt, A, b, c)))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    last = sum(lens) - 1  # what is left is the last token's addend
+    want = (torch.logaddexp(R.f64(dt[last, 1]), torch.zeros(()).double()) * R.f64(x[last, 1]))[:, None] * R.f64(b[last, 0])
+    R.assert_within(out[1][0][-1, 1], want, 16 * R.U32 * want.abs() + 1e-38, "state")
