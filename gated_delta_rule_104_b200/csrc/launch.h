@@ -188,6 +188,12 @@ cudaError_t launch_ssm_join(const SsmParams &p, const SeqIdx &q, const SsmSegs &
 cudaError_t read_ssm_faults(unsigned int *out, bool clear);
 size_t ssm_work_bytes(int T, int n_seq, int H, int dk, int dv);
 
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float ex2_ftz(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

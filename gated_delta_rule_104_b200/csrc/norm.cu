@@ -16,13 +16,6 @@ namespace dl {
 
 namespace {
 
-// max that keeps a NaN: a group with one gets scale NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 template <int N>
 __device__ __forceinline__ void load_n(const float *p, float (&x)[N]) {
     if constexpr (N == 1)

@@ -261,7 +261,7 @@ struct Steps {
             // (a step of e^-128 is 0 in fp32 as any stronger one is; kept there, sums over 32
             // tokens stay within 4096, and the exponential of a difference of two is off by
             // at most 2^-10 behind any number of such steps: a quarter of a bf16 rounding)
-            l[j] = w[j] = in ? fmaxf(dt[j] * A, -128.f) : 0.f;
+            l[j] = w[j] = in ? max_nan(dt[j] * A, -128.f) : 0.f;
         }
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1)

@@ -110,3 +110,32 @@ def test_ssm_prompt_of_a_head_that_forgets_at_once(g, lens, dv, dtype):
     last = sum(lens) - 1  # what is left is the last token's addend
     want = (torch.logaddexp(R.f64(dt[last, 1]), torch.zeros(()).double()) * R.f64(x[last, 1]))[:, None] * R.f64(b[last, 0])
     R.assert_within(out[1][0][-1, 1], want, 16 * R.U32 * want.abs() + 1e-38, "state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dv", [64, 128])
+@pytest.mark.parametrize("lens", CALLS, ids=str)
+def test_ssm_prompt_of_a_decay_that_is_no_number(g, lens, dv, dtype):
+    """A of NaN: nothing of that head is a number. A step size of infinity under A = 0
+    (0 times infinity): nothing of it from there on. Other heads and sequences stay as they were."""
+    H, dk, T = 3, 64, sum(lens)
+    x, dt, A, b, c = layer_inputs(32, T, H, dk, dv, dtype)
+    A[0] = 0.0
+
+    def run():
+        S = torch.ones(len(lens), H, dv, dk, device="cuda")
+        return S, prompt(g, S, lens, x, dt, A, b, c)
+
+    S0, y0 = run()
+    used = [i for i, n in enumerate(lens) if n]
+    A[1] = float("nan")
+    S, y = run()
+    assert bool(S[used, 1].isnan().all()) and bool(y[:, 1].isnan().all())
+    assert torch.equal(S[:, ::2], S0[:, ::2]) and torch.equal(y[:, ::2], y0[:, ::2])
+    A[1] = -1.0
+    S0, y0 = run()
+    at = T - 3  # in the last sequence
+    dt[at, 0] = float("inf")
+    S, y = run()
+    assert bool(S[-1, 0].isnan().all()) and bool(y[at:, 0].isnan().all()) and torch.equal(y[:at], y0[:at])
+    assert torch.equal(S[:, 1:], S0[:, 1:]) and torch.equal(S[:-1], S0[:-1]) and torch.equal(y[:, 1:], y0[:, 1:])
