@@ -52,6 +52,9 @@ __device__ __forceinline__ void store_n(bf16 *p, const float (&x)[N]) {
     }
 }
 
+// The scale of a group whose largest |y| is m: NaN where m is no finite number.
+__device__ __forceinline__ float scale_of(float m, float top) { return m <= 3.402823466e38f ? m / top : __int_as_float(0x7fffffff); }
+
 // x / scale correctly rounded: by the row's reciprocal where i8_fast(scale)
 // (see i8_code), else by division; 0 for scale 0.
 template <bool FAST>
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     const float top = i8 ? 127.f : 448.f;
     uint8_t *y = static_cast<uint8_t *>(p.y) + row * width;
     if (p.group == 0) {
-        const float scale = row_reduce<true>(m, red[1]) / top;
+        const float scale = scale_of(row_reduce<true>(m, red[1]), top);
         if (live && threadIdx.x == 0) p.scale[row] = scale;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
             for (int c = 4 * g; c < 4 * g + 4; ++c) gm = max_nan(gm, fabsf(h[c][0]));
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) gm = max_nan(gm, __shfl_xor_sync(0xffffffffu, gm, off));
-            const float scale = gm / top;
+            const float scale = scale_of(gm, top);
             const int gi = g * nw + warp;
             if (live && lane == 0 && gi < groups) p.scale[row * groups + gi] = scale;
 #pragma unroll
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
             for (int e = 0; e < VEC; ++e) gm = max_nan(gm, fabsf(h[c][e]));
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1) gm = max_nan(gm, __shfl_xor_sync(0xffffffffu, gm, off));
-            const float scale = gm / top;
+            const float scale = scale_of(gm, top);
             const int col = column(c);
             if (live && col < width) {
                 if (col % 128 == 0) p.scale[row * groups + col / 128] = scale;

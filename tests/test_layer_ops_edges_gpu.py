@@ -48,6 +48,35 @@ def prompt(g, S, lens, x, dt, A, b, c, **k):
     return y
 
 
+# ------------------------------------------------------------------ norm
+
+@pytest.mark.parametrize("out", [torch.int8, torch.float8_e4m3fn])
+@pytest.mark.parametrize("width", [512, 511])
+def test_norm_scale_of_an_infinite_value(g, width, out):
+    """A value behind the weight that is infinite (an infinite weight, a product past float32): its group has scale
+    NaN, as with a NaN, and reads back as no number; other groups are as without it."""
+    x = torch.randn(4, width, generator=gen(33), device="cuda")
+    for group in (0, 128):
+        got = []
+        for high in (1.0, 3e38, float("inf")):
+            w = torch.ones(width, device="cuda")
+            w[200] = high
+            x[:, 200] = 2.0  # (its norm is above 1.2)
+            y = torch.zeros(4, width, dtype=out, device="cuda")
+            scale = torch.zeros(4, 4 if group else 1, device="cuda")
+            g.dl_rms_norm(x, w, 1e-6, y, scale=scale, group=group)
+            v = torch.zeros(4, width, device="cuda")
+            g.dl_rows_from_8bit(y, scale, v, group=group)
+            got.append((scale, v))
+        bad = slice(128, 256) if group else slice(0, width)
+        keep = [k for k in range(width) if not (bad.start <= k < bad.stop)]
+        for scale, v in got[1:]:
+            assert bool(scale[:, 1 if group else 0].isnan().all()) and bool(v[:, bad].isnan().all())
+            assert torch.equal(v[:, keep], got[0][1][:, keep])
+            if group:
+                assert torch.equal(scale[:, [0, 2, 3]], got[0][0][:, [0, 2, 3]])
+
+
 # ------------------------------------------------------------------ decays of the tensor-core scan
 
 @pytest.mark.parametrize("strong", [16, 40, 100, 112, 120])
