@@ -463,22 +463,22 @@ def dl_pool_flush(pool: Pool, slot, stream=None) -> None:
 # (These calls take a dozen tensors and a kernel of a few microseconds: what is
 # checked of a tensor is checked in one function, by the cheapest queries.)
 
-_codes = _getdevice = _getstream = _i32 = None
+_found = None
 
 
-def _queries() -> None:
-    """The device, the stream and the dtypes of torch, looked up once."""
-    global _codes, _getdevice, _getstream, _i32
+def _queries():
+    """torch's dtypes -> dl_dtype, its queries of the current device and of a device's current stream, and its int32:
+    looked up once, and set together, so that another thread's first call sees all of them or none."""
+    global _found
     torch = _torch()
-    _getdevice, _getstream, _i32 = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, torch.int32
-    _codes = {torch.float32: DL_F32, torch.bfloat16: DL_BF16, torch.int8: DL_I8, torch.float8_e4m3fn: DL_E4M3}
+    codes = {torch.float32: DL_F32, torch.bfloat16: DL_BF16, torch.int8: DL_I8, torch.float8_e4m3fn: DL_E4M3}
+    _found = codes, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, torch.int32
+    return _found
 
 
 def _code_of(t) -> int:
     """dl_dtype of a tensor (as _dtype_code, 8-bit types too)."""
-    if _codes is None:
-        _queries()
-    code = _codes.get(t.dtype)
+    code = (_found or _queries())[0].get(t.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
     return code
@@ -498,9 +498,7 @@ def _float_code(*ts) -> int:
 
 def _device() -> int:
     """The current device: a call launches there, and every operand must lie on it."""
-    if _getdevice is None:
-        _queries()
-    return _getdevice()
+    return (_found or _queries())[1]()
 
 
 def _misplaced(t, name: str, dev: int):
@@ -510,7 +508,7 @@ def _misplaced(t, name: str, dev: int):
 
 
 def _raw_stream(stream, dev: int) -> int:
-    return _getstream(dev) if stream is None else _stream(stream)
+    return (_found or _queries())[2](dev) if stream is None else _stream(stream)
 
 
 def _full(t, name: str, shape, dev: int) -> int:
@@ -528,7 +526,7 @@ def _f32(t, name: str, shape, dev: int) -> Optional[int]:
     """The same of a float32 tensor, or None."""
     if t is None:
         return None
-    if _codes.get(t.dtype) != DL_F32:
+    if (_found or _queries())[0].get(t.dtype) != DL_F32:
         raise TypeError(f"{name} must be float32, got {t.dtype}")
     return _full(t, name, shape, dev)
 
@@ -554,7 +552,7 @@ def _index(t, name: str, n: int, dev: int) -> Optional[int]:
     """Pointer of an int32 tensor of n elements, or None."""
     if t is None:
         return None
-    if t.dtype is not _i32:
+    if t.dtype is not (_found or _queries())[3]:
         raise TypeError(f"{name} must be int32, got {t.dtype}")
     return _full(t, name, (n,), dev)
 
