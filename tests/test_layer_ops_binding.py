@@ -1,5 +1,6 @@
 """Host-side checks of the binding of the norm, the short convolution and the
 selective scan, with stand-ins for torch and for tensors (no GPU)."""
+import math
 import types
 
 import pytest
@@ -39,3 +40,59 @@ def test_first_calls_of_two_threads(monkeypatch, k):
     assert b._device() == 3
     call()
     assert set(seen) == {(3, 43, 128, 64, b.DL_BF16)}
+
+
+class Stand:
+    """What the binding asks of a contiguous tensor on the current device, of any size."""
+
+    is_cuda = True
+
+    def __init__(self, shape, dtype, ptr):
+        self.shape, self.dtype, self._ptr = tuple(shape), dtype, ptr
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self._ptr
+
+    def numel(self):
+        return math.prod(self.shape)
+
+
+OVER = 2 ** 32 + 64  # its lower 32 bits are a size that every call takes
+
+
+def test_sizes_past_31_bits_are_refused(monkeypatch):
+    """Sizes that do not fit the C ABI's int: a row of that width, that many tokens, channels, slots and sequences."""
+    torch = pytest.importorskip("torch")
+    f32, i8, i32 = torch.float32, torch.int8, torch.int32
+    monkeypatch.setattr(b, "_found", ({f32: b.DL_F32, i8: b.DL_I8}, lambda: 0, lambda dev: 0, i32))
+    place = iter(range(1, 1000))
+    t = lambda *shape, dtype=f32: Stand(shape, dtype, (1 << 46) + (next(place) << 38))  # noqa: E731
+
+    def conv(step, rows=8, channels=64, P=OVER - 60, n=2):
+        x, w, state, y = t(rows, channels), t(channels, 4), t(P, 3, channels), t(rows, channels)
+        if step:
+            b.dl_conv_step(x, w, None, state, None, y)
+        else:
+            b.dl_conv_prompt(x, w, None, state, t(n + 1, dtype=i32), None, y)
+
+    def scan(n):
+        S, x, v = t(4, 1, 64, 64), t(8, 1, 64), t(8, 1, 64)
+        b.dl_ssm_prompt(S, t(n + 1, dtype=i32), None, x, t(8, 1), t(1), v, v, t(8, 1, 64))
+
+    calls = [lambda: b.dl_rms_norm(t(1, OVER), t(OVER), 1e-5, t(1, OVER)),
+             lambda: b.dl_rows_from_8bit(t(1, OVER, dtype=i8), t(1), t(1, OVER)),
+             lambda: conv(False, rows=OVER), lambda: conv(False, channels=OVER), lambda: conv(False), lambda: conv(True),
+             lambda: conv(True, rows=OVER, P=OVER), lambda: conv(False, P=4, n=2 ** 32 + 2), lambda: scan(2 ** 32 + 2),
+             lambda: b.dl_ssm_work_bytes(OVER, 1, 1, 64, 64)]
+    for call in calls:
+        with pytest.raises(ValueError, match="exceeds 2"):
+            call()
