@@ -439,6 +439,8 @@ static dl_status seq_checks(const int *seq_start, bool ragged, int n_seq, int T,
     if (n_seq < 1) return fail(DL_ERR_INVALID_ARG, "the number of sequences (%d) must be >= 1", n_seq);
     if (P < n_seq) return fail(DL_ERR_INVALID_ARG, "%d sequences need distinct slots but P=%d", n_seq, P);
     if (T < 0) return fail(DL_ERR_INVALID_ARG, "T=%d is negative", T);
+    // tiles of 8 rows or more are numbered in 32 bits (see seq_index.h)
+    if (ragged && (long long)T / 8 + n_seq >= 0x7fffffffLL) return fail(DL_ERR_UNSUPPORTED, "T / 8 + n_seq exceeds 2^31 - 2");
     b[0] = {"seq_start", seq_start, ((size_t)n_seq + 1) * sizeof(int), 4, !ragged};
     b[1] = {"slot", slot, (size_t)n_seq * sizeof(int), 4, slot == nullptr};
     b[2] = {"status", status, sizeof(int), 4, status == nullptr};
