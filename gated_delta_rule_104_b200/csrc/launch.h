@@ -10,6 +10,7 @@
 
 #include "../../include/deltalog.h"
 #include "common.cuh"
+#include "pairs.cuh"
 #include "seq_index.h"
 
 namespace dl {

@@ -61,6 +61,7 @@
 #include "guard.cuh"
 #include "merge_tc_layout.h"
 #include "tc.cuh"
+#include "tensor_map.h"
 
 namespace dl {
 

@@ -49,7 +49,8 @@
 // Every wait is bounded (about 2 s, fault bit 0).
 #include "launch.h"
 #include "ssm_tc_layout.h"
-#include "tc.cuh"
+#include "tc_scan.cuh"
+#include "tensor_map.h"
 
 namespace dl {
 
