@@ -42,6 +42,16 @@ def test_first_calls_of_two_threads(monkeypatch, k):
     assert set(seen) == {(3, 43, 128, 64, b.DL_BF16)}
 
 
+def test_a_torch_without_its_own_queries(monkeypatch):
+    """The public queries stand in for the ones that a torch need not have."""
+    torch = types.SimpleNamespace(
+        _C=types.SimpleNamespace(), float32=1, bfloat16=2, int8=3, float8_e4m3fn=4, int32=5,
+        cuda=types.SimpleNamespace(current_device=lambda: 6, current_stream=lambda dev: types.SimpleNamespace(cuda_stream=70 + dev)))
+    monkeypatch.setattr(b, "_found", None)
+    monkeypatch.setattr(b, "_torch", lambda: torch)
+    assert b._device() == 6 and b._raw_stream(None, 6) == 76
+
+
 class Stand:
     """What the binding asks of a contiguous tensor on the current device, of any size."""
 
