@@ -35,3 +35,18 @@ def _index_guard_clean(request):
     assert g.dl_index_guard_build(), "the index-guard library is not the one loaded"
     flags = g.dl_device_faults(clear=True)
     assert not (flags & 2), "index guard: " + g.load().dl_last_error().decode()
+
+
+@pytest.fixture(autouse=True)
+def _no_bounded_wait_ran_out(request):
+    """After each GPU test of the norm, the convolution and the scan, whatever its name: no kernel gave up a wait."""
+    yield
+    if not request.node.path.name.startswith("test_layer_ops") or request.node.get_closest_marker("gpu") is None:
+        return
+    import torch
+
+    if not torch.cuda.is_available():
+        return
+    import gated_delta_rule_104_b200 as g
+
+    assert g.dl_device_faults(clear=True) == 0, "a bounded wait ran out"
