@@ -43,3 +43,22 @@ def test_two_parts_of_an_addend_do_not_reach_a_float32_state(dv):
     assert float((off > 4 * R.U32 * f.abs()).double().mean()) > 0.5
     third = (f.float() - part.float() - second.float()).to(torch.bfloat16)
     assert bool(((part.double() + second.double() + third.double() - f).abs() <= 2 * R.U32 * f.abs()).all())
+
+
+# ------------------------------------------------------------------ the workspace
+
+def test_a_workspace_that_does_not_fit_is_refused(lib):
+    """One long sequence on few heads needs a workspace: given too small, missing, misaligned or inside another operand, it is refused."""
+    T, H, dk, dv = 1 << 16, 6, 64, 128
+    need = lib.dl_ssm_work_bytes(T, 1, H, dk, dv)
+    assert need > 0
+    m = b.dl_ssm(addr(3), H * dv, addr(4), H, addr(5), dk, addr(6), dk, None, 0, addr(7), None, None, b.DL_BF16)
+
+    def call(work, size):
+        status = lib.dl_ssm_prompt(addr(0), b.DL_F32, 1, None, None, ctypes.byref(m), addr(1), 1, T, addr(2), H, 1, dk, dv, work, size, None)
+        return status, lib.dl_last_error().decode()
+
+    for work, size, text in ((addr(8), need - 1, "work holds"), (None, need, "work is a null"), (addr(8) + 8, need, "aligned"),
+                             (addr(2) + 4096, need, "overlaps")):
+        status, error = call(work, size)
+        assert status == b.DL_ERR_INVALID_ARG and text in error
