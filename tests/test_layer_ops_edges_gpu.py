@@ -188,3 +188,65 @@ def test_ssm_prompt_keeps_a_float32_state_to_its_last_bits(g, n, dv):
         want = f[:, :, None] * R.f64(b1)
         R.assert_within(S[0], want, 4 * R.U32 * want.abs(), f"state, token {at} of {n}")
 
+
+# ------------------------------------------------------------------ strides, alignment, options
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dv", [64, 128])
+@pytest.mark.parametrize("lens", CALLS + [[1] * 5], ids=str)
+def test_ssm_of_slices_of_wider_rows(g, lens, dv, dtype):
+    """Every operand a slice of rows that are wider than it, dt at an odd offset of rows of odd width: as
+    contiguous ones, to the bit. (Sequences of one token each by the single step too.)"""
+    H, G, dk, T = 4, 2, 64, sum(lens)
+    rng = gen(34)
+    widths = [("x", H, dv), ("z", H, dv), ("b", G, dk), ("c", G, dk)]
+    rows = torch.randn(T, 32 + sum(h * d + 8 for _, h, d in widths), generator=rng, device="cuda").to(dtype)
+    loose, first = {}, 16
+    for name, h, d in widths:
+        loose[name] = rows[:, first:first + h * d].unflatten(1, (h, d))
+        first += h * d + 8
+    loose["dt"] = torch.randn(T, 2 * H + 3, generator=rng, device="cuda").to(dtype)[:, 3:3 + H] - 1
+    wide = torch.zeros(T, 2 * H + 3, dtype=dtype, device="cuda")
+    wide[:, 3:3 + H] = loose["dt"]
+    loose["dt"] = wide[:, 3:3 + H]
+    A = -1 - 8 * torch.rand(H, generator=rng, device="cuda")
+    D = torch.randn(H, generator=rng, device="cuda")
+    assert not any(v.is_contiguous() for v in loose.values())
+    tight = {k: v.contiguous() for k, v in loose.items()}
+    out = []
+    for m in (loose, tight):
+        S = torch.ones(len(lens), H, dv, dk, device="cuda")
+        y = prompt(g, S, lens, m["x"], m["dt"], A, m["b"], m["c"], D=D, z=m["z"])
+        out.append([S, y])
+        if max(lens) == 1:
+            S, y = torch.ones_like(S), torch.zeros_like(y)
+            g.dl_ssm_step(S, None, m["x"], m["dt"], A, m["b"], m["c"], y, D=D, z=m["z"])
+            out[-1] += [S, y]
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert bool((out[0][1] != 7).any()) and bool(out[0][1].isfinite().all())
+    r = R.scan(torch.ones(H, dv, dk), *[tight[k][:lens[0]] for k in ("x", "dt")], A, tight["b"][:lens[0]], tight["c"][:lens[0]], D,
+               None, tight["z"][:lens[0]])  # (the first sequence; the roundings of the tensor cores' products as elsewhere)
+    bound = 12 * R.U32 * r["y_err"] + (dk + 64) * R.U32 * r["y_mag"] + 2 * R.half_step(dtype) * (r["y_mag"] + r["y"].abs()) + 1e-38
+    R.assert_within(out[0][1][:lens[0]], r["y"], bound, "y")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("taps", [2, 3, 4])
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("off", [0, 1])
+def test_conv_bias_at_any_alignment_and_no_activation(g, off, silu, taps, dtype):
+    """A bias that no 16-byte access fits beside wide rows, and sums without the activation, over prompts and by single tokens."""
+    C, n = 264, 21
+    rng = gen(35 + taps)
+    bias = torch.randn(C + 8, generator=rng, device="cuda").to(dtype)[off:off + C]
+    x, w = torch.randn(n, C, generator=rng, device="cuda").to(dtype), torch.randn(C, taps, generator=rng, device="cuda").to(dtype)
+    hist = torch.randn(1, taps - 1, C, generator=rng, device="cuda").to(dtype)
+    want, mag = R.conv(torch.cat([hist[0], x]), w, bias, silu)
+    bound = 1.1 * (taps + 2) * R.U32 * mag + (64 * R.U32 + R.half_step(dtype)) * want.abs() + 1e-38
+    y, state = torch.zeros_like(x), hist.clone()
+    g.dl_conv_prompt(x, w, bias, state, starts([n]), None, y, silu=silu)
+    R.assert_within(y, want, bound, "prompt")
+    single, history = torch.zeros_like(x), hist.clone()
+    for t in range(n):
+        g.dl_conv_step(x[t:t + 1], w, bias, history, None, single[t:t + 1], silu=silu)
+    assert torch.equal(single, y) and torch.equal(history, state)
