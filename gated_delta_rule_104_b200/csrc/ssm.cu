@@ -26,8 +26,9 @@ constexpr int STEP_R = 8;  // state loads a lane has in flight
 // loads in flight per lane before any arithmetic, a shuffle sum per row, no
 // shared memory. A lane holds x, z and y of one of the unit's rows, which keeps a
 // float32 state's kernel within the 64 registers of four blocks an SM (256
-// sequences of 32 heads of 128 x 128: 157 us; 187 with each row's x loaded by its
-// lanes and three blocks, 177 with four rows' loads in flight).
+// sequences of 32 heads of 128 x 128: 166 us of the 164 that the state's bytes take;
+// 198 with each row's x loaded by its lanes and three blocks, 177 with four rows'
+// loads in flight; all three a pass through the binding).
 template <class ST, class IT, int DK>
 __global__ void __launch_bounds__(256, sizeof(ST) == 4 ? 4 : 3) ssm_step_kernel(const SsmParams p, const SeqIdx q, long long num_units) {
     constexpr int VEC = StateVec<ST>::N, G = DK / VEC, RPW = 32 / G, R = STEP_R, UNIT = R * RPW;

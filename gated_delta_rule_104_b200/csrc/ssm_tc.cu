@@ -13,13 +13,16 @@
 //   S' = exp(l_end) S + W^T B, W = X o weights, K = tokens
 //
 // What is rounded: x, b and c are bfloat16 and enter as they are. P and the
-// state read by C S^T are rounded to bfloat16 once (2^-9 of each term, where y
-// itself is rounded to 2^-9); the addends W go in as three bfloat16 parts, 24
-// bits, so that the state, accumulated and kept in fp32, keeps fp32's accuracy
-// (two parts, 2^-17 of each term, where the state is stored as bfloat16). Every exponent is <= 0: between 32-token blocks the
-// decay is split at the end of the earlier token's block, inside a block it is
-// taken directly. The weights' exponents are sums from the chunk's end
-// backwards, so a token's weight is as accurate as its own exponent is small.
+// state read by C S^T are rounded to bfloat16 once (at most 2^-8 of each term, as
+// y itself): they are operands of a bf16 product, and y's own rounding hides most
+// of it (y's mean error grows by an eighth). The addends W go in as three bfloat16
+// parts (at most 2^-26 left), so that the state, accumulated and kept in fp32,
+// keeps fp32's accuracy; two parts (2^-17) where the state is stored as bfloat16.
+// Every exponent is <= 0: between blocks of 32 tokens the decay is split at the end
+// of the earlier token's block, inside a block it is taken directly, and sums of
+// log decays run over no more than a block (see Scal). The weights' exponents are
+// sums from the chunk's end backwards, so a token's weight is as accurate as its
+// own exponent is small.
 //
 // One block per (sequence, 128 value rows): one head's, or two heads' of 64
 // that share b and c. It walks the chunks in order with S in tensor memory:
@@ -35,14 +38,18 @@
 // times that: 3100 a chunk in all. What the other warps issue is as much, so
 // their loops are short (unrolled over a tile they waited for instructions five
 // cycles for each one issued: 320 us where the loops took 234 us, before other
-// changes). A chunk takes 5300 cycles, bound by the chain from G over P to P X
-// with y's epilogue behind it and by the issue slots (11000 with a gate and two
-// heads of 64): 8 ragged prompts of 16263 tokens on 32 heads of 128 x 128 take
-// 153 us, where moving their bytes takes 47.
+// changes). With every SM at work a chunk takes 6450 cycles (3.4 us; 3.7 in long
+// runs, in which the clock falls to 1.73 GHz), bound by the chain from G over P to
+// P X with y's epilogue behind it and by the issue slots; 10600 with a gate, 8700
+// for two heads of 64, 12000 for two with a gate. 8 ragged prompts of 16263 tokens
+// on 32 heads of 128 x 128, the longest of 40 chunks, take 153 us, where moving
+// their bytes takes 47: 40 chunks, and 15 us for the first loads and the last stores.
+// The kernels of end states and join, which find nothing to do there, are 12 more.
 //
 // What is not a number stays where the recurrence has it: products would
 // spread it, as a weight of zero times NaN is NaN. Rows behind the segment are
-// zeroed in X and B; an x that is no finite number is zeroed in X (after W has
+// zeroed in X and B (G may read B meanwhile: what it makes of those rows reaches
+// rows of y behind the segment only, which are not stored); an x that is no finite number is zeroed in X (after W has
 // taken it) and its row flagged, and y's owners of later rows add it back from
 // global memory.
 //

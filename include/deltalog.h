@@ -334,11 +334,19 @@ dl_status dl_state_from_i8(const void *S_i8, void *S, dl_dtype s_dtype,
  *              i): the slots of one call must be distinct. A row whose slot is
  *              outside [0, P) is skipped (no output, no state written) and ORs
  *              1 into *status (status may be null), so a batch padded for a
- *              captured graph names slot -1 in its padding rows.
+ *              captured graph names slot -1 in its padding rows. A call has
+ *              at most P sequences, those padding rows among them.
+ *   No rows    T = 0 (or rows = 0) does nothing: nothing is launched, and
+ *              *status stays as it is.
  *   Stream     one call's results do not depend on other calls' work unless
  *              they share a slot or a workspace; such calls must be ordered by
  *              the caller. Every sum has a fixed order: the same call gives the
  *              same bits.
+ *   Numerics   sums and states are fp32 (a bf16 state is rounded when it is
+ *              stored), each output is rounded once. u / (1 + exp(-u)) uses the
+ *              hardware's exponential and reciprocal where the output is bf16
+ *              (2^-18 relative for |u| <= 16; 0 below u = -87), the accurate
+ *              ones where it is fp32.
  */
 
 /* Root-mean-square norm of rows, with the residual's addition:
@@ -394,8 +402,9 @@ typedef struct {
  *           read as the tokens before the sequence and replaced by its own last
  *           taps - 1 (zeros for a new sequence)
  *   y       [T, channels]
- * T >= 0 and n_seq >= 1. Pointers need only their element's alignment; 16-byte
- * aligned rows of a multiple of 16 bytes take the wide path. */
+ * T >= 0, n_seq >= 1, T / 8 + n_seq <= 2^31 - 2. Pointers need only their
+ * element's alignment; 16-byte aligned rows of a multiple of 16 bytes take the
+ * wide path. */
 dl_status dl_conv_prompt(const dl_conv *conv, const void *x, long long x_stride, int T,
                          const int *seq_start, int n_seq,
                          void *state, int P, const int *slot, int *status,
@@ -414,7 +423,8 @@ dl_status dl_conv_step(const dl_conv *conv, const void *x, long long x_stride, i
  * with S in R^{d_v x d_k}, x, y, z in R^{d_v}, b, c in R^{d_k}: the head-wise decay
  * of the steps above with k = b, q = c, v = dt x and no delta correction.
  * Vector rows (x, b, c, z) must start at 16-byte boundaries (pointer and row
- * stride); dt needs only its element's alignment. A must be <= 0. */
+ * stride); dt needs only its element's alignment. A must be <= 0 (-inf: a head
+ * that forgets at once). */
 typedef struct {
     const void *x;        /* [rows, H, d_v], row stride x_stride */
     long long x_stride;
@@ -444,7 +454,20 @@ size_t dl_ssm_work_bytes(int T, int n_seq, int H, int d_k, int d_v);
  *   work dl_ssm_work_bytes(...) bytes, 16-byte aligned (null if that is 0),
  *        contents irrelevant between calls (calls that may run at the same
  *        time need one each)
- * T >= 0, n_seq >= 1, G divides H. */
+ * T >= 0, n_seq >= 1, G divides H.
+ * Numerics. fp32 inputs, and bf16 ones with few tokens a sequence (about 24), are
+ * advanced token by token in fp32. Other bf16 prompts run on the tensor cores:
+ *   - the scores (c_t . b_s) times decay and step, and the state as c reads it, are
+ *     rounded to bf16 (at most 2^-8 of each term), also under an fp32 state: y is
+ *     off by up to 2^-7 of its terms' magnitudes beside its own rounding (by an
+ *     eighth more than that on average);
+ *   - the state's addends are held to 2^-26 (fp32 state) or 2^-17 (bf16 state);
+ *   - a step's log decay below -128 counts as -128 (either leaves 0 in fp32), and a
+ *     decay behind such steps is off by at most 2^-10.
+ * Which of the two runs, and whether a long sequence is cut into segments that are
+ * joined in fp32, depends on T, n_seq, H and d_v: a sequence's last bits may differ
+ * between calls that lay other sequences or other padding rows beside it. A caller
+ * that needs y in fp32 accuracy passes fp32 inputs. */
 dl_status dl_ssm_prompt(void *S, dl_dtype s_dtype, int P, const int *slot, int *status,
                         const dl_ssm *in, const int *seq_start, int n_seq, int T,
                         void *y, int H, int G, int d_k, int d_v,
