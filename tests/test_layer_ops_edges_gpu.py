@@ -2,9 +2,15 @@
 edges of their contract, beside test_layer_ops_gpu.py. References in 64 bits;
 u = 2^-24 is half a float32 step, relative, and a rounding to bfloat16 is off by
 at most 2^-8 of the value as R.half_step counts it."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 from tests import layer_ref as R
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 torch = pytest.importorskip("torch")
 
@@ -250,3 +256,80 @@ def test_conv_bias_at_any_alignment_and_no_activation(g, off, silu, taps, dtype)
     for t in range(n):
         g.dl_conv_step(x[t:t + 1], w, bias, history, None, single[t:t + 1], silu=silu)
     assert torch.equal(single, y) and torch.equal(history, state)
+
+
+# ------------------------------------------------------------------ two calls at once, first calls in a capture
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_calls_on_two_streams_at_once(g, dtype):
+    """Scans, convolutions and norms queued on two streams together, each with its own state and workspace: as one after the other."""
+    H, dk, dv = 4, 64, 64
+    lens = [[3000], [700, 40, 1500]]
+    calls = []
+    for k, n in enumerate(lens):
+        x, dt, A, b, c = layer_inputs(40 + k, sum(n), H, dk, dv, dtype)
+        calls.append((n, x, dt, A, b, c, torch.randn(H * dv, 4, generator=gen(42 + k), device="cuda").to(dtype), starts(n),
+                      torch.empty(g.dl_ssm_work_bytes(sum(n), len(n), H, dk, dv), dtype=torch.uint8, device="cuda")))
+
+    def run(n, x, dt, A, b, c, w, seq, work, out):
+        rows = x.view(sum(n), H * dv)
+        g.dl_rms_norm(rows, torch.ones(H * dv, device="cuda"), 1e-5, out["n"])
+        g.dl_conv_prompt(out["n"], w, None, out["h"], seq, None, out["u"])
+        g.dl_ssm_prompt(out["S"], seq, None, out["u"].view(sum(n), H, dv), dt, A, b, c, out["y"], work=work)
+
+    def buffers(n):
+        z = lambda *s, t=dtype: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+        T = sum(n)
+        return dict(n=z(T, H * dv), u=z(T, H * dv), h=z(len(n), 3, H * dv), S=z(len(n), H, dv, dk, t=F32), y=z(T, H, dv))
+
+    want = [buffers(n) for n in lens]
+    for args, out in zip(calls, want):
+        run(*args, out)
+    streams = [torch.cuda.Stream() for _ in lens]
+    for _ in range(5):
+        got = [buffers(n) for n in lens]
+        torch.cuda.synchronize()
+        for args, out, stream in zip(calls, got, streams):
+            with torch.cuda.stream(stream):
+                run(*args, out)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[k], b[k]) for a, b in zip(got, want) for k in a)
+
+
+FIRST = """
+import torch, sys
+import gated_delta_rule_104_b200 as g
+dtype = getattr(torch, sys.argv[1])
+T, H, d = 300, 2, 64
+z = lambda *s, t=dtype: torch.zeros(*s, dtype=t, device="cuda")
+x = torch.randn(T, H * d, device="cuda").to(dtype)
+seq = torch.tensor([0, 130, T], dtype=torch.int32, device="cuda")
+one, w, A, dt, b = torch.ones(H * d, device="cuda"), torch.randn(H * d, 4, device="cuda").to(dtype), -torch.ones(H, device="cuda"), z(T, H), x.view(T, H, d)[:, :1].contiguous()
+work = torch.empty(max(1, g.dl_ssm_work_bytes(T, 2, H, d, d)), dtype=torch.uint8, device="cuda")
+o = [dict(q=z(T, H * d, t=torch.int8), s=z(T, t=torch.float32), v=z(T, H * d), u=z(T, H * d), h=z(2, 3, H * d), S=z(2, H, d, d, t=torch.float32), y=z(T, H, d), y1=z(2, H, d), u1=z(2, H * d)) for _ in range(2)]
+def run(o):
+    g.dl_rms_norm(x, one, 1e-5, o["q"], scale=o["s"])
+    g.dl_rows_from_8bit(o["q"], o["s"], o["v"])
+    g.dl_conv_prompt(o["v"], w, None, o["h"], seq, None, o["u"])
+    g.dl_ssm_prompt(o["S"], seq, None, o["u"].view(T, H, d), dt, A, b, b, o["y"], work=work)
+    g.dl_conv_step(o["v"][:2], w, None, o["h"], None, o["u1"])
+    g.dl_ssm_step(o["S"], None, o["u1"].view(2, H, d), dt[:2], A, b[:2], b[:2], o["y1"])
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    run(o[0])
+graph.replay()
+torch.cuda.synchronize()
+run(o[1])
+torch.cuda.synchronize()
+assert all(torch.equal(o[0][k], o[1][k]) for k in o[0]) and g.dl_device_faults() == 0 and bool((o[0]["y1"] != 0).any())
+del graph
+print("same")
+"""
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_the_first_calls_of_a_process_in_a_capture(dtype):
+    """Nothing that a first call sets up is forbidden while a graph is captured."""
+    out = subprocess.run([sys.executable, "-c", FIRST, dtype], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr
