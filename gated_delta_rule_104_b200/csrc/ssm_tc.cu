@@ -387,6 +387,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         for (int k = 0; k < W_PLACES; ++k) init(W_FULL + k, 4);
         for (int b : {(int)P_READY, (int)Y_FREE}) init(b, 8);
         for (int k = 0; k < LY::NXQ; ++k) init(X_FREE + k, 2);
+        init(Y_DONE, 2);
         for (int k = 0; k < 2; ++k) {
             init(SC_FULL + k, NH);
             init(SC_FREE + k, 20);
@@ -859,6 +860,9 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                 if (!(ok = update(W_PLACES, 8))) break;
                 tc::mma_commit_by(lead, &bars[ST_DONE]);
                 tc::mma_commit_by(lead, &bars[B_FREE + par]);
+                // (a commit speaks for products only: this arrival passes on x and its flags, of
+                // which the addends' barriers told, to the warps that wait for y)
+                tc::mbar_arrive_by(lead, &bars[Y_DONE]);
                 if (!(ok = wait_warp(&bars[P_READY], par, abort) && wait_warp(&bars[YS_READY], par, abort))) break;
                 tc::tc_fence_after();
 #pragma unroll
@@ -943,7 +947,7 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     if (tid == 0) {
         for (int b = 0; b < BARS; ++b) {
             const bool sc_full = b >= SC_FULL && b < SC_FREE, sc_free = b >= SC_FREE && b < W_FULL, w_full = b >= W_FULL && b < W_FREE;
-            tc::mbar_init(&bars[b], sc_full ? NH : sc_free ? 16 : w_full ? 4 : 1);
+            tc::mbar_init(&bars[b], sc_full ? NH : sc_free ? 16 : w_full ? 4 : b >= FREE && b < X_FULL ? 2 : 1);
         }
         *abort = 0;
         tc::mbar_init_fence();
@@ -1049,7 +1053,10 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                         tc::mma_ts_f16_by(lead, tb + T_S, tb + T_W8 + W_PLACE * g + 8 * i, bd + g * ROWS, ID_S, c + g + i > 0);
                     tc::mma_commit_by(lead, &bars[W_FREE + g]);
                 }
-                if (ok) tc::mma_commit_by(lead, &bars[FREE + k]);  // (W of the chunk has been made, so x has been read too)
+                if (ok) {
+                    tc::mma_commit_by(lead, &bars[FREE + k]);
+                    tc::mbar_arrive_by(lead, &bars[FREE + k]);  // (W of the chunk has been made, so x has been read too)
+                }
             }
             tc::mma_commit_by(lead, &bars[DONE]);
             if (!ok) drain(&bars[DONE], 0);

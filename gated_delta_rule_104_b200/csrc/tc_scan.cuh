@@ -33,7 +33,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) 
                  : "memory");
 }
 
-// mma_ss_f16 and mma_ts_f16, called by a converged warp and issued by its lane with `lead` set: the
+// mma_ss_f16, mma_ts_f16, mbar_arrive and mma_commit, called by a converged warp and issued by its lane with `lead` set: the
 // operands stay in uniform registers, where a branch around the call would move
 // each of them there first (120 cycles to issue instead of the product's 64).
 __device__ __forceinline__ void mma_ss_f16_by(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -50,6 +50,12 @@ __device__ __forceinline__ void mma_ts_f16_by(uint32_t lead, uint32_t d_tmem, ui
         "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_by(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit_by(uint32_t lead, uint64_t *bar) {

@@ -6,13 +6,16 @@ products, synchronised by mbarriers whose waits name a phase by its parity.
 Products run behind their issue. A commit's barrier is signalled once every
 product issued before it has completed; products with the same accumulator
 complete in the order of their issue, others in any order. Nothing else orders a
-product with respect to another one or to a warp that writes what it reads.
+product with respect to another one or to a warp that writes what it reads. And a
+commit speaks for products only: copies, and what a warp wrote or has read itself,
+are known to those who wait for a barrier on which the copy or the warp arrived, or
+another warp that knew of it.
 
-The order in which the product warp waits, issues and commits is read from the
-kernel's source; the other roles are written out with its index and parity
+The order in which the product warp waits, issues, commits and arrives is read from
+the kernel's source; the other roles are written out with its index and parity
 formulas. All are interleaved at random, with some of the warps held back and with products
-and copies that complete late. Whatever is read must hold the chunk it is meant to, nothing
-may be written while a product or a copy in flight reads or writes it, every wait
+and copies that complete late. Whatever is read must hold the chunk it is meant to and
+be known to the reader, nothing may be written while a product or a copy in flight reads or writes it, every wait
 that passes must be for the phase it meant, and every warp must finish.
 """
 import os
@@ -28,7 +31,7 @@ LATE = (0.004, 0.05, 0.5)  # how often a product or copy completes rather than a
 
 def product_steps():
     """What the product warp does in a chunk, in the order of the source: ("wait", barrier, phase, not in the first
-    chunk), ("issue", product), ("update", first, last), ("commit", barrier)."""
+    chunk), ("issue", product), ("update", first, last), ("commit", barrier), ("arrive", barrier)."""
     with open(SOURCE, encoding="utf-8") as f:
         text = f.read()
     kernel = text[text.index("ssm_tc_kernel("):text.index("ssm_tc_ends_kernel(")]
@@ -41,7 +44,7 @@ def product_steps():
     part = part[z + len("return true;"):]
     pattern = (r"(?P<first>c == 0 \|\| )?wait_warp\(&bars\[(?P<wait>\w+)(?: \+ par)?\], (?P<phase>par2|par|\(c - 1\) & 1), abort\)"
                r"|over_columns\(tb \+ (?P<over>T_G|T_Y)|update\((?P<lo>\w+), (?P<hi>\w+)\)|mma_ts_f16_by\(lead, tb \+ (?P<px>T_Y)"
-               r"|mma_commit_by\(lead, &bars\[(?P<commit>\w+)(?: \+ par)?\]\)")
+               r"|mma_commit_by\(lead, &bars\[(?P<commit>\w+)(?: \+ par)?\]\)|mbar_arrive_by\(lead, &bars\[(?P<arrive>\w+)\]\)")
     number = {"W_PLACES": W_PLACES, "0": 0, "8": 8}
     steps = []
     for m in re.finditer(pattern, part):
@@ -53,8 +56,10 @@ def product_steps():
             steps.append(("update", number[m["lo"]], number[m["hi"]]))
         elif m["px"]:
             steps.append(("issue", "PX"))
-        else:
+        elif m["commit"]:
             steps.append(("commit", m["commit"]))
+        else:
+            steps.append(("arrive", m["arrive"]))
     assert [s[1] for s in steps if s[0] == "issue"] == ["G", "CS", "PX"]
     assert [s[1:] for s in steps if s[0] == "update"] == [(0, W_PLACES), (W_PLACES, 8)]
     assert len(re.findall(r"wait_warp\(", part)) == sum(s[0] == "wait" for s in steps)
@@ -65,9 +70,11 @@ def product_steps():
 class Barrier:
     def __init__(self, count):
         self.count, self.pending, self.done = count, count, 0
+        self.known = set()  # what who waits for it learns
 
-    def arrive(self):
+    def arrive(self, known=()):
         self.pending -= 1
+        self.known |= set(known)
         assert self.pending >= 0
         if self.pending == 0:
             self.done += 1
@@ -82,7 +89,7 @@ class Block:
         self.steps, self.chunks, self.nh, self.nxq = steps, chunks, nh, nxq
         self.rng = random.Random(seed)
         one = ["C_FULL", "C_FREE", "G_DONE", "Y2_DONE", "Y_DONE", "ST_DONE"]
-        self.bars = {k: Barrier(1) for k in one}
+        self.bars = {k: Barrier(1 + steps.count(("arrive", k))) for k in one}
         self.bars |= {k: Barrier(4) for k in ("S_READY", "YS_READY")} | {k: Barrier(8) for k in ("P_READY", "Y_FREE")}
         for k in range(2):
             self.bars |= {("B_FULL", k): Barrier(1), ("B_FREE", k): Barrier(1), ("SC_FULL", k): Barrier(nh), ("SC_FREE", k): Barrier(20)}
@@ -143,12 +150,14 @@ class Block:
             place, what, bar = self.copies.pop(k - len(ready))[:3]
             if bar is not None:
                 self.holds[place] = what
-                self.bars[bar].arrive()
+                self.bars[bar].arrive([(place[0], what)])
 
-    def wait(self, bar, parity, phase):
+    def wait(self, bar, parity, phase, known=None):
         while not self.bars[bar].passes(parity):
             yield
         assert self.bars[bar].done == phase, (bar, self.bars[bar].done, phase)
+        if known is not None:
+            known |= self.bars[bar].known
 
     def load(self, place, what, bar):
         assert not any(place in p["reads"] for p in self.flying) and not any(c[0] == place for c in self.copies), place
@@ -167,6 +176,9 @@ class Block:
                 nc += 1
             xp = nx % self.nxq
             if nx < 4 * self.chunks and (nx < self.nxq or self.bars["X_FREE", xp].passes((nx // self.nxq - 1) & 1)):
+                if nx >= self.nxq:
+                    known = self.bars["X_FREE", xp].known
+                    assert all(("taken", nx - self.nxq, q, h) in known for q in range(4) for h in (0, 1)), "x loaded over its readers"
                 self.load(("x", xp), nx, ("X_FULL", xp))
                 nx += 1
             yield
@@ -184,7 +196,7 @@ class Block:
             assert self.holds["scalars", c & 1, h] == c
 
     def scores(self, quad, half):
-        stored = []
+        stored, known = [], set()
         for c in range(self.chunks):
             yield from self.wait(("SC_FULL", c & 1), (c // 2) & 1, c // 2 + 1)
             yield from self.wait("G_DONE", c & 1, c + 1)
@@ -197,11 +209,14 @@ class Block:
                 while any(s in self.copies for s in stored):  # its stores have read x's place
                     yield
                 stored = []
-                self.bars["X_FREE", (4 * (c - 1) + quad) % self.nxq].arrive()
-            yield from self.wait("Y_DONE", c & 1, c + 1)
+                self.bars["X_FREE", (4 * (c - 1) + quad) % self.nxq].arrive(known)
+            yield from self.wait("Y_DONE", c & 1, c + 1, known)
             self.read("y", ("whole", c))
             place = ("x", (4 * c + quad) % self.nxq)
-            assert self.holds[place] == 4 * c + quad
+            assert self.holds[place] == 4 * c + quad and ("x", 4 * c + quad) in known, "x read without a word of its copy"
+            for q in range(4):
+                for h in (0, 1):
+                    assert self.holds["flags", c % 3, q, h] == c and ("flags", c, q, h) in known, "flags read without a word of them"
             assert not any(place in p["reads"] for p in self.flying), "x overwritten under a product"
             yield
             self.bars["Y_FREE"].arrive()
@@ -229,6 +244,7 @@ class Block:
             yield
 
     def addends(self, quad, half):
+        known = set()
         for c in range(self.chunks):
             yield from self.wait(("SC_FULL", c & 1), (c // 2) & 1, c // 2 + 1)
             self.scalars(c, range(self.nh))
@@ -236,18 +252,22 @@ class Block:
                 nx = 4 * c + q
                 nw = 2 * nx + half
                 place = nw % W_PLACES
-                yield from self.wait(("X_FULL", nx % self.nxq), (nx // self.nxq) & 1, nx // self.nxq + 1)
+                yield from self.wait(("X_FULL", nx % self.nxq), (nx // self.nxq) & 1, nx // self.nxq + 1, known)
+                assert ("x", nx) in known
                 self.read(("x", nx % self.nxq), nx)
+                known.add(("taken", nx, quad, half))
                 if nw >= W_PLACES:
                     yield from self.wait(("W_FREE", place), (nw // W_PLACES - 1) & 1, nw // W_PLACES)
                 self.write(("w", place, quad), nw)
+                self.holds["flags", c % 3, quad, half] = c
+                known.add(("flags", c, quad, half))
                 if q == 3:
                     self.bars["SC_FREE", c & 1].arrive()
-                self.bars["W_FULL", place].arrive()
+                self.bars["W_FULL", place].arrive(known)
                 yield
 
     def products(self):
-        quads = range(4)
+        quads, known = range(4), set()
         for c in range(self.chunks):
             for step in self.steps:
                 if step[0] == "wait":
@@ -269,11 +289,13 @@ class Block:
                     for g in range(step[1], step[2]):
                         nw = 8 * c + g
                         place = nw % W_PLACES
-                        yield from self.wait(("W_FULL", place), (nw // W_PLACES) & 1, nw // W_PLACES + 1)
+                        yield from self.wait(("W_FULL", place), (nw // W_PLACES) & 1, nw // W_PLACES + 1, known)
                         self.issue("s", {("w", place, q): nw for q in quads} | {("b", c & 1): c} | {("s", q): ("decayed", c) for q in quads},
                                    {"s": ("updated", c)})
                         yield
                         self.commit(("W_FREE", place))
+                elif step[0] == "arrive":
+                    self.bars[step[1]].arrive(known)
                 else:
                     self.commit((step[1], c & 1) if step[1] == "B_FREE" else step[1])
                 yield
@@ -313,3 +335,10 @@ def test_the_model_notices_each_wait_that_is_left_out(barrier):
     with pytest.raises(AssertionError):
         for seed in range(24):
             Block(steps, 7, 1, 11, seed).run(late=LATE[seed % 3])
+
+
+def test_the_model_notices_an_arrival_that_is_left_out():
+    """What the product warp passes on beside its commits."""
+    steps = [s for s in product_steps() if s[0] != "arrive"]
+    with pytest.raises(AssertionError, match="without a word"):
+        Block(steps, 2, 1, 11, 0).run(late=0.5)
