@@ -48,8 +48,8 @@
 //
 // What is not a number stays where the recurrence has it: products would
 // spread it, as a weight of zero times NaN is NaN. Rows behind the segment are
-// zeroed in X and B (G may read B meanwhile: what it makes of those rows reaches
-// rows of y behind the segment only, which are not stored); an x that is no finite number is zeroed in X (after W has
+// zeroed in X and B (after G, in which they reach only rows of y that are not
+// stored); an x that is no finite number is zeroed in X (after W has
 // taken it) and its row flagged, and y's owners of later rows add it back from
 // global memory.
 //
@@ -707,7 +707,8 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             const uint32_t par = c & 1, par2 = (c >> 1) & 1;
             const int m = min(Q, len - c * Q);
             if (!wait_warp(&bars[SC_FULL + par], par2, abort)) break;
-            if (m < Q && !wait_warp(&bars[B_FULL + par], par2, abort)) break;
+            // (the last chunk: b has come, and the scores have been formed from it, before its rows behind the segment are zeroed)
+            if (m < Q && !(wait_warp(&bars[B_FULL + par], par2, abort) && wait_warp(&bars[G_DONE], par, abort))) break;
             const float *w = scal(c, h) + Scal::W;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {  // 32 tokens, this set's 16 of them

@@ -18,6 +18,7 @@ and copies that complete late. Whatever is read must hold the chunk it is meant 
 be known to the reader, nothing may be written while a product or a copy in flight reads or writes it, every wait
 that passes must be for the phase it meant, and every warp must finish.
 """
+import functools
 import os
 import random
 import re
@@ -65,6 +66,15 @@ def product_steps():
     assert len(re.findall(r"wait_warp\(", part)) == sum(s[0] == "wait" for s in steps)
     assert len(re.findall(r"mma_commit_by\(", part)) == sum(s[0] == "commit" for s in steps)
     return steps
+
+
+@functools.cache
+def zeroing_waits():
+    """What a warp of the addends waits for before it zeroes b behind the segment, in the last chunk."""
+    with open(SOURCE, encoding="utf-8") as f:
+        text = f.read()
+    text = text[text.index("ssm_tc_kernel("):]
+    return re.findall(r"wait_warp\(&bars\[(\w+)", re.search(r"if \(m < Q && ([^\n]*)", text)[1])
 
 
 class Barrier:
@@ -248,6 +258,13 @@ class Block:
         for c in range(self.chunks):
             yield from self.wait(("SC_FULL", c & 1), (c // 2) & 1, c // 2 + 1)
             self.scalars(c, range(self.nh))
+            if c == self.chunks - 1:
+                assert set(zeroing_waits()) <= {"B_FULL", "G_DONE"}
+                if "B_FULL" in zeroing_waits():
+                    yield from self.wait(("B_FULL", c & 1), (c // 2) & 1, c // 2 + 1, known)
+                if "G_DONE" in zeroing_waits():
+                    yield from self.wait("G_DONE", c & 1, c + 1)
+                assert ("b", c) in known, "b zeroed before it came"
             for q in range(4):
                 nx = 4 * c + q
                 nw = 2 * nx + half
@@ -256,6 +273,8 @@ class Block:
                 assert ("x", nx) in known
                 self.read(("x", nx % self.nxq), nx)
                 known.add(("taken", nx, quad, half))
+                if c == self.chunks - 1:
+                    assert self.bars["G_DONE"].done == c + 1, "b zeroed while the scores may read it"
                 if nw >= W_PLACES:
                     yield from self.wait(("W_FREE", place), (nw // W_PLACES - 1) & 1, nw // W_PLACES)
                 self.write(("w", place, quad), nw)
