@@ -514,10 +514,11 @@ def _raw_stream(stream, dev: int) -> int:
     return (_found or _queries())[2](dev) if stream is None else _stream(stream)
 
 
-def _ints(*sizes) -> None:
-    """Refuses sizes that the C ABI's int does not hold (ctypes would drop their upper bits)."""
-    if max(sizes) > 0x7fffffff:
-        raise ValueError(f"a size of {max(sizes)} exceeds 2^31 - 1")
+_INT = 0x7fffffff  # the C ABI's largest int: ctypes would drop the upper bits of a larger one
+
+
+def _too_large(*sizes):
+    return ValueError(f"a size of {max(sizes)} exceeds 2^31 - 1")
 
 
 def _full(t, name: str, shape, dev: int) -> int:
@@ -577,7 +578,8 @@ def dl_rms_norm(x, weight, eps: float, y, residual=None, residual_out=None, scal
         raise ValueError("x must be [rows, width]")
     dev = _device() if x.is_cuda else -2
     rows, width = shape = x.shape
-    _ints(width)
+    if width > _INT:
+        raise _too_large(width)
     xp, xs = _rows(x, "x", shape, dev, width)
     xc, yc = _float_code(x), _code_of(y)
     if (residual is None) != (residual_out is None):
@@ -610,7 +612,8 @@ def dl_rows_from_8bit(codes, scale, out, group: int = 0, stream=None) -> None:
         raise ValueError("codes must be [rows, width]")
     dev = _device() if codes.is_cuda else -2
     rows, width = shape = codes.shape
-    _ints(width)
+    if width > _INT:
+        raise _too_large(width)
     status = load().dl_rows_from_8bit(_full(codes, "codes", shape, dev), _code_of(codes), _scales(scale, rows, width, group, dev),
                                       group, _full(out, "out", shape, dev), _float_code(out), rows, width,
                                       _raw_stream(stream, dev))
@@ -623,7 +626,8 @@ def _conv(x, w, bias, state, y, silu, dev):
         raise ValueError("x must be [rows, channels], w [channels, taps], state [P, taps - 1, channels]")
     rows, channels = shape = x.shape
     taps, P = w.shape[1], state.shape[0]
-    _ints(rows, channels, taps, P)
+    if (rows | channels | taps | P) > _INT:
+        raise _too_large(rows, channels, taps, P)
     xp, xs = _rows(x, "x", shape, dev, channels)
     cv = dl_conv(_full(w, "w", (channels, taps), dev), None if bias is None else _full(bias, "bias", (channels,), dev), channels,
                  taps, _float_code(x, w, bias, state, y), 1 if silu else 0)
@@ -638,7 +642,8 @@ def dl_conv_prompt(x, w, bias, state, seq_start, slot, y, silu: bool = True, sta
     dev = _device() if x.is_cuda else -2
     cv, xp, xs, T, sp, P, yp = _conv(x, w, bias, state, y, silu, dev)
     n = seq_start.numel() - 1
-    _ints(n)
+    if n > _INT:
+        raise _too_large(n)
     st = load().dl_conv_prompt(ctypes.byref(cv), xp, xs, T, _index(seq_start, "seq_start", n + 1, dev), n, sp, P,
                                _index(slot, "slot", n, dev), _index(status, "status", 1, dev), yp, _raw_stream(stream, dev))
     if st:
@@ -660,7 +665,8 @@ def _ssm(S, x, dt, A, b, c, y, D, dt_bias, z, dev):
         raise ValueError("S must be [P, H, d_v, d_k], x [rows, H, d_v], b and c [rows, G, d_k]")
     P, H, dv, dk = s_shape = S.shape
     rows, G = x.shape[0], b.shape[1]
-    _ints(P, H, dv, dk, rows, G)
+    if (P | H | dv | dk | rows | G) > _INT:
+        raise _too_large(P, H, dv, dk, rows, G)
     wide, keys, heads = (rows, H, dv), (rows, G, dk), (H,)
     zp, zs = (None, 0) if z is None else _rows(z, "z", wide, dev, H * dv)
     xp, xs = _rows(x, "x", wide, dev, H * dv)
@@ -676,7 +682,8 @@ def _ssm(S, x, dt, A, b, c, y, D, dt_bias, z, dev):
 
 def dl_ssm_work_bytes(T: int, n_seq: int, H: int, d_k: int, d_v: int) -> int:
     """Bytes of workspace dl_ssm_prompt needs (0 if none)."""
-    _ints(T, n_seq, H, d_k, d_v)
+    if max(T, n_seq, H, d_k, d_v) > _INT:
+        raise _too_large(T, n_seq, H, d_k, d_v)
     return int(load().dl_ssm_work_bytes(int(T), int(n_seq), int(H), int(d_k), int(d_v)))
 
 
@@ -690,7 +697,8 @@ def dl_ssm_prompt(S, seq_start, slot, x, dt, A, b, c, y, D=None, dt_bias=None, z
     dev = _device() if x.is_cuda else -2
     m, P, H, G, dk, dv, T, yp, Sp, sc = _ssm(S, x, dt, A, b, c, y, D, dt_bias, z, dev)
     n = seq_start.numel() - 1
-    _ints(n)
+    if n > _INT:
+        raise _too_large(n)
     wp, wb = None, 0
     if work is not None and work.numel():
         wp, wb = _full(work, "work", work.shape, dev), work.numel() * work.element_size()
