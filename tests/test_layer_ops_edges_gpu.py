@@ -333,3 +333,53 @@ def test_the_first_calls_of_a_process_in_a_capture(dtype):
     """Nothing that a first call sets up is forbidden while a graph is captured."""
     out = subprocess.run([sys.executable, "-c", FIRST, dtype], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_a_captured_call_replayed_on_other_lengths_and_slots(g, dv, dtype):
+    """Lengths and slots are read on the device: a graph captured over some is replayed over others, padding rows and
+    sequences without a slot among them, as a call made for those."""
+    H, dk, T, P = 2, 64, 3000, 6
+    x, dt, A, b, c = layer_inputs(50, T, H, dk, dv, dtype)
+    rows, w = x.view(T, H * dv), torch.randn(H * dv, 4, generator=gen(51), device="cuda").to(dtype)
+    seq, slot = torch.zeros(5, dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    work = torch.empty(g.dl_ssm_work_bytes(T, 4, H, dk, dv), dtype=torch.uint8, device="cuda")
+    fresh = lambda: dict(S=torch.ones(P, H, dv, dk, device="cuda"), h=torch.ones(P, 3, H * dv, dtype=dtype, device="cuda"),  # noqa: E731
+                         y=torch.full_like(x, 7.0), u=torch.full_like(rows, 7.0),
+                         status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+
+    def run(o):
+        g.dl_conv_prompt(rows, w, None, o["h"], seq, slot, o["u"], status=o["status"])
+        g.dl_ssm_prompt(o["S"], seq, slot, x, dt, A, b, c, o["y"], work=work, status=o["status"])
+
+    calls = [([0, 700, 700, 2900, 3000], [3, 1, 0, 5]), ([0, 2999, 2999, 2999, 2999], [5, -1, -1, -1]),
+             ([100, 101, 129, 2000, 2600], [0, 2, 4, 1]), ([0, 0, 0, 0, 0], [0, 1, 2, 3])]
+    seq.copy_(torch.tensor(calls[0][0]))
+    slot.copy_(torch.tensor(calls[0][1]))
+    cap, graph = fresh(), torch.cuda.CUDAGraph()
+    run(fresh())
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        run(cap)
+    for start, slots in calls:
+        seq.copy_(torch.tensor(start))
+        slot.copy_(torch.tensor(slots))
+        want = fresh()
+        for k, v in want.items():
+            cap[k].copy_(v)
+        run(want)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(cap[k], want[k]) for k in cap) and int(cap["status"]) == (1 if -1 in slots else 0)
+        assert bool((cap["y"][:start[0]] == 7).all()) and bool((cap["y"][start[-1]:] == 7).all())
+        for i, k in enumerate(slots):
+            n = start[i + 1] - start[i]
+            if k >= 0 and n:
+                at = slice(start[i], start[i + 1])
+                r = R.scan(torch.ones(H, dv, dk), x[at], dt[at], A, b[at], c[at], None, None, None)
+                off = 12 * R.U32 * r["S_err"] + (2.0 ** -16 if dtype == BF16 else R.U32) * r["S_mag"] + 1e-38
+                R.assert_within(cap["S"][k], r["S"], off, "state")
+            elif k >= 0:
+                assert bool((cap["S"][k] == 1).all())
+    del graph
