@@ -350,7 +350,7 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
               const __grid_constant__ CUtensorMap map_z, const __grid_constant__ Args a) {
     using LY = Layout<DK, NH, GATE>;
     constexpr int X_FREE = X_FULL + LY::NXQ, BARS = X_FREE + LY::NXQ;
-    static_assert(LY::N_BAR == BARS, "barriers");
+    static_assert(LY::N_BAR == BARS && BARS <= 128, "barriers");
     // parts of the addends: 24 bits under an fp32 state, 16 under a bfloat16 one
     constexpr int TERMS = sizeof(ST) == 4 ? 3 : 2;
     extern __shared__ uint8_t smem_raw[];
@@ -380,19 +380,12 @@ ssm_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     const int len = min(a.seg_len, n - seg * a.seg_len);  // this segment's tokens, from row0
     const int row0 = s0 + seg * a.seg_len, chunks = (len + Q - 1) / Q;
 
-    if (tid == 0) {
-        auto init = [&](int b, int count) { tc::mbar_init(&bars[b], count); };
-        for (int b = 0; b < BARS; ++b) init(b, 1);
-        for (int b : {(int)S_READY, (int)YS_READY}) init(b, 4);
-        for (int k = 0; k < W_PLACES; ++k) init(W_FULL + k, 4);
-        for (int b : {(int)P_READY, (int)Y_FREE}) init(b, 8);
-        for (int k = 0; k < LY::NXQ; ++k) init(X_FREE + k, 2);
-        init(Y_DONE, 2);
-        for (int k = 0; k < 2; ++k) {
-            init(SC_FULL + k, NH);
-            init(SC_FREE + k, 20);
-        }
-        *abort = 0;
+    if (tid < BARS) {  // (a thread each, and each once: a second init of a live barrier is undefined)
+        const int b = tid;
+        const bool four = b == S_READY || b == YS_READY || (b >= W_FULL && b < W_FREE), eight = b == P_READY || b == Y_FREE;
+        const bool sc_full = b >= SC_FULL && b < SC_FREE, sc_free = b >= SC_FREE && b < Z_FULL, two = b == Y_DONE || b >= X_FREE;
+        tc::mbar_init(&bars[b], four ? 4 : eight ? 8 : sc_full ? NH : sc_free ? 20 : two ? 2 : 1);
+        if (b == 0) *abort = 0;
         tc::mbar_init_fence();
     }
     if (warp == 21) {
@@ -923,7 +916,7 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     enum { B_FULL, FREE = B_FULL + LY::ST, X_FULL = FREE + LY::ST, SC_FULL = X_FULL + LY::ST, SC_FREE = SC_FULL + 2, W_FULL = SC_FREE + 2,
            W_FREE = W_FULL + 8, DONE = W_FREE + 8, BARS };  // (a place of W for each 16 tokens of a chunk)
     constexpr int T_W8 = 256;
-    static_assert(LY::N_BAR == BARS, "barriers");
+    static_assert(LY::N_BAR == BARS && BARS <= 128, "barriers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + LY::BAR);
@@ -945,12 +938,11 @@ ssm_tc_ends_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const int row0 = s0 + seg * a.seg_len, chunks = a.seg_len / Q;
     const long long out = (long long)seg_base(s0, a.seg_len) + seg;
 
-    if (tid == 0) {
-        for (int b = 0; b < BARS; ++b) {
-            const bool sc_full = b >= SC_FULL && b < SC_FREE, sc_free = b >= SC_FREE && b < W_FULL, w_full = b >= W_FULL && b < W_FREE;
-            tc::mbar_init(&bars[b], sc_full ? NH : sc_free ? 16 : w_full ? 4 : b >= FREE && b < X_FULL ? 2 : 1);
-        }
-        *abort = 0;
+    if (tid < BARS) {
+        const int b = tid;
+        const bool sc_full = b >= SC_FULL && b < SC_FREE, sc_free = b >= SC_FREE && b < W_FULL, w_full = b >= W_FULL && b < W_FREE;
+        tc::mbar_init(&bars[b], sc_full ? NH : sc_free ? 16 : w_full ? 4 : b >= FREE && b < X_FULL ? 2 : 1);
+        if (b == 0) *abort = 0;
         tc::mbar_init_fence();
     }
     if (warp == 17) {

@@ -361,3 +361,15 @@ def test_the_model_notices_an_arrival_that_is_left_out():
     steps = [s for s in product_steps() if s[0] != "arrive"]
     with pytest.raises(AssertionError, match="without a word"):
         Block(steps, 2, 1, 11, 0).run(late=0.5)
+
+
+@pytest.mark.parametrize("kernel", ["ssm_tc_kernel(", "ssm_tc_ends_kernel("])
+def test_every_barrier_is_set_up_once(kernel):
+    """One mbarrier.init each: on a barrier that has been set up, a second one is undefined."""
+    with open(SOURCE, encoding="utf-8") as f:
+        text = f.read()
+    text = text[text.index(kernel):]
+    setup = text[:text.index("tc::mbar_init_fence()")]
+    setup = setup[setup.rindex("    if (tid "):]
+    assert len(re.findall(r"\binit\(|mbar_init\(", setup)) == 1 and "for (" not in setup
+    assert setup.lstrip().startswith("if (tid < BARS) {") and "const int b = tid;" in setup and "mbar_init(&bars[b]," in setup
